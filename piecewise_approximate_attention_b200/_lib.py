@@ -17,12 +17,15 @@ PISA_OK, PISA_ERR_INVALID_ARG, PISA_ERR_UNSUPPORTED, PISA_ERR_CUDA, PISA_ERR_DEV
 PISA_BF16, PISA_FP32, PISA_BF16_FP8QK = 0, 1, 2
 PISA_MODE_PISA, PISA_MODE_EXACT_ONLY, PISA_MODE_PER_BLOCK = 0, 1, 2
 PISA_DEVERR_WAIT_TIMEOUT, PISA_DEVERR_BAD_SELECTION = 1, 2
+PISA_DEVERR_BAD_PAGE, PISA_DEVERR_BAD_LENGTH = 3, 4
+PISA_CACHE_BF16, PISA_CACHE_FP32, PISA_CACHE_E4M3 = 0, 1, 2
 
 SYMBOLS = ("pisa_abi_version", "pisa_num_blocks", "pisa_stats_bytes", "pisa_stats_carve", "pisa_workspace_bytes",
            "pisa_precompute", "pisa_route", "pisa_attention", "pisa_read_device_error", "pisa_status_string",
            "pisa_precompute_noalloc", "pisa_testing_set_attention_fault", "pisa_perblock_workspace_bytes",
            "pisa_permute_rows", "pisa_axis_permutation", "pisa_precompute_zeroth_order", "pisa_precompute_route",
-           "pisa_testing_set_precompute_fault")
+           "pisa_testing_set_precompute_fault", "pisa_cache_workspace_bytes", "pisa_cache_append", "pisa_cache_read",
+           "pisa_cache_attention")
 
 
 class PisaShape(ctypes.Structure):
@@ -35,6 +38,23 @@ class PisaStats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("qbar", "kbar", "vsum", "hbar", "M", "H", "kbar_op", "vsum_op", "hbar_op", "v_op", "vscale",
                  "hdiff_op", "q8", "k8", "kbar8", "qscale", "kscale", "kbscale")]
+
+
+class PisaCache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)]
+
+
+class PisaSequences(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("counts", ctypes.c_void_p)]
+
+
+class PisaRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int32), ("seq_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class PisaError(RuntimeError):
@@ -75,6 +95,11 @@ def lib() -> ctypes.CDLL:
             "pisa_testing_set_attention_fault": (i32, [i32, ctypes.c_uint64]),
             "pisa_testing_set_precompute_fault": (i32, [i32, ctypes.c_uint64]),
             "pisa_permute_rows": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp]),
+            "pisa_cache_workspace_bytes": (sz, [P(PisaCache)]),
+            "pisa_cache_append": (i32, [P(PisaCache), P(PisaSequences), P(PisaRows), P(PisaRows), vp, sz, vp]),
+            "pisa_cache_read": (i32, [P(PisaCache), P(PisaSequences), P(PisaRows), P(PisaRows), vp, sz, vp]),
+            "pisa_cache_attention": (i32, [P(PisaCache), P(PisaSequences), i32, i32, i32, f32, P(PisaRows), P(PisaRows),
+                                           vp, vp, sz, vp]),
             "pisa_axis_permutation": (i32, [i32, i32, i32, i32, ctypes.c_char_p, P(i32), ctypes.c_int64]),
         }
         for name, (res, args) in sig.items():
@@ -262,6 +287,36 @@ def pisa_axis_permutation(grid, order: str, extra_tokens: int = 0):
                                        out.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), out.size),
            "pisa_axis_permutation")
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# Paged key/value cache (include/pisa_cache.h)
+# ---------------------------------------------------------------------------------------------
+def rows_of(x, packed: bool) -> PisaRows:
+    """The token tensor x, packed [T, heads, d] or padded [B, heads, L, d], any strides with a contiguous last axis."""
+    if packed:
+        t, h, _ = x.stride()
+        return PisaRows(x.data_ptr(), x.shape[0], 0, t, h)
+    b, h, t, _ = x.stride()
+    return PisaRows(x.data_ptr(), x.shape[2], b, t, h)
+
+
+def pisa_cache_workspace_bytes(cache: PisaCache) -> int:
+    return int(lib().pisa_cache_workspace_bytes(ctypes.byref(cache)))
+
+
+def pisa_cache_append(cache: PisaCache, seqs: PisaSequences, k: PisaRows, v: PisaRows, ws, stream=None):
+    _check(lib().pisa_cache_append(cache, seqs, k, v, _ptr(ws), ws.numel(), _stream(stream)), "pisa_cache_append")
+
+
+def pisa_cache_read(cache: PisaCache, seqs: PisaSequences, k: PisaRows, v: PisaRows, ws, stream=None):
+    _check(lib().pisa_cache_read(cache, seqs, k, v, _ptr(ws), ws.numel(), _stream(stream)), "pisa_cache_read")
+
+
+def pisa_cache_attention(cache: PisaCache, seqs: PisaSequences, heads: int, causal: bool, window: int,
+                         softmax_scale: float, q: PisaRows, o: PisaRows, lse, ws, stream=None):
+    _check(lib().pisa_cache_attention(cache, seqs, heads, causal, window, softmax_scale, q, o, _ptr(lse), _ptr(ws),
+                                      ws.numel(), _stream(stream)), "pisa_cache_attention")
 
 
 def pisa_read_device_error(ws, stream=None):

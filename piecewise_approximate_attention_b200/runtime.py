@@ -112,6 +112,133 @@ class Pisa:
         return C.pisa_read_device_error(self.ws, stream)
 
 
+class Sequences:
+    """Which tokens a call on a PagedCache is about; made by PagedCache.sequences, reusable for any
+    number of calls (every layer of a step) while its tensors hold what is meant."""
+
+    def __init__(self, c, packed: bool, total: int, tensors):
+        self.c, self.packed, self.total, self.tensors = c, packed, total, tensors
+
+
+class PagedCache:
+    """Keys and values of earlier tokens in pages of ``page`` tokens, for ``heads`` query heads on
+    ``kv_heads`` key/value heads (pisa_cache.h): ``append`` stores new tokens, ``read`` gives stored
+    tokens back dense, ``attention`` lets new tokens attend over them.
+
+    ``dtype``: "bf16", "fp32", or "e4m3" (8-bit codes with a power-of-two scale per token and head,
+    for bf16 tokens).  The pool tensors ``k``, ``v`` [num_pages, kv_heads, page, head_dim] (uint8 codes
+    for e4m3) and ``k_exp``, ``v_exp`` [num_pages, kv_heads, page] (uint8) are allocated here unless given.
+    One workspace: calls on one PagedCache must not run at the same time on the device.
+    """
+
+    DTYPES = {"bf16": C.PISA_CACHE_BF16, "fp32": C.PISA_CACHE_FP32, "e4m3": C.PISA_CACHE_E4M3}
+
+    def __init__(self, num_pages: int, heads: int, kv_heads: int, page: int, head_dim: int, dtype: str = "bf16",
+                 device="cuda", k=None, v=None, k_exp=None, v_exp=None):
+        import torch
+        if dtype not in self.DTYPES:
+            raise ValueError(f"dtype must be one of {sorted(self.DTYPES)}")
+        if heads < 1 or kv_heads < 1 or heads % kv_heads:
+            raise ValueError("heads must be a multiple of kv_heads")
+        self.num_pages, self.heads, self.kv_heads, self.page, self.head_dim = num_pages, heads, kv_heads, page, head_dim
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.tdtype = torch.float32 if dtype == "fp32" else torch.bfloat16
+        self.fp8 = dtype == "e4m3"
+        sizes = C.PisaCache(num_pages, kv_heads, page, head_dim, self.DTYPES[dtype])
+        n = C.pisa_cache_workspace_bytes(sizes)
+        if n == 0:
+            raise C.PisaError(C.PISA_ERR_UNSUPPORTED, "pisa_cache_workspace_bytes")
+        shape = (num_pages, kv_heads, page, head_dim)
+        pool = torch.uint8 if self.fp8 else self.tdtype
+
+        def buffer(x, shape, dtype, name):
+            if x is None:
+                return torch.zeros(shape, dtype=dtype, device=self.device)
+            if tuple(x.shape) != shape or x.dtype != dtype or x.device != self.device or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}")
+            return x
+
+        self.k, self.v = buffer(k, shape, pool, "k"), buffer(v, shape, pool, "v")
+        self.k_exp = buffer(k_exp, shape[:3], torch.uint8, "k_exp") if self.fp8 else None
+        self.v_exp = buffer(v_exp, shape[:3], torch.uint8, "v_exp") if self.fp8 else None
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self.c = C.PisaCache(num_pages, kv_heads, page, head_dim, self.DTYPES[dtype], C._ptr(self.k), C._ptr(self.v),
+                             C._ptr(self.k_exp), C._ptr(self.v_exp))
+
+    def sequences(self, page_table, lens, max_len: int, max_new: int, starts=None, counts=None) -> Sequences:
+        """``page_table`` [batch, pages] and ``lens`` [batch] (new tokens included), int32 on the
+        cache's device; ``max_len`` and ``max_new`` are upper bounds of the lengths and of a sequence's
+        new tokens.  ``starts`` [batch + 1]: the sequences' rows in packed token tensors; else the token
+        tensors are padded, with ``counts`` [batch] new tokens each (``max_new`` each if None)."""
+        import torch
+        batch = lens.shape[0]
+        want = [(page_table, "page_table", 2, batch), (lens, "lens", 1, batch), (starts, "starts", 1, batch + 1),
+                (counts, "counts", 1, batch)]
+        for x, name, dims, n in want:
+            if x is not None and (x.dtype != torch.int32 or x.device != self.device or x.dim() != dims or
+                                  x.shape[0] != n or not x.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} axes and {n} rows on {self.device}")
+        if starts is not None and counts is not None:
+            raise ValueError("starts (packed) and counts (padded) exclude one another")
+        c = C.PisaSequences(batch, page_table.shape[1], max_len, max_new, C._ptr(page_table), C._ptr(lens),
+                            C._ptr(starts), C._ptr(counts))
+        return Sequences(c, starts is not None, batch, (page_table, lens, starts, counts))
+
+    def _rows(self, seqs: Sequences, x, heads: int, name: str):
+        if (x.dtype != self.tdtype or x.device != self.device or x.shape[-1] != self.head_dim or x.stride(-1) != 1 or
+                x.shape[1] != heads):
+            raise ValueError(f"{name} must be a {self.tdtype} tensor on {self.device} with {heads} heads of "
+                             f"{self.head_dim} contiguous elements")
+        if x.dim() != (3 if seqs.packed else 4) or (not seqs.packed and x.shape[0] != seqs.total):
+            raise ValueError(f"{name} must be [tokens, heads, d] (packed) or [batch, heads, rows, d] (padded)")
+        return C.rows_of(x, seqs.packed)
+
+    def _call(self, fn, args, stream):
+        """On the cache's device, whatever the current one is."""
+        import torch
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache is on {self.device}: the kernels take CUDA tensors only")
+        if self.device.index == torch.cuda.current_device():
+            fn(*args, self.ws, stream)
+        else:
+            with torch.cuda.device(self.device):
+                fn(*args, self.ws, stream)
+
+    def append(self, seqs: Sequences, k, v, stream=None):
+        """Stores the new tokens' k and v (kv_heads heads) in their pages."""
+        self._call(C.pisa_cache_append, (self.c, seqs.c, self._rows(seqs, k, self.kv_heads, "k"),
+                                         self._rows(seqs, v, self.kv_heads, "v")), stream)
+
+    def read(self, seqs: Sequences, k, v, stream=None):
+        """Writes each sequence's last tokens (counts or starts say how many) from the pages into k and v."""
+        self._call(C.pisa_cache_read, (self.c, seqs.c, self._rows(seqs, k, self.kv_heads, "k"),
+                                       self._rows(seqs, v, self.kv_heads, "v")), stream)
+
+    def attention(self, seqs: Sequences, q, o=None, causal: bool = True, window: int = 0, softmax_scale: float = 1.0,
+                  lse=None, stream=None):
+        """Attention of the new tokens' q (heads heads) over their sequence's cached tokens, into o.
+        ``causal``: no later token is seen; ``window`` > 0: only keys less than that far back.  ``lse``
+        (fp32, [tokens, heads] packed or [batch, heads, rows] padded) takes the log of the softmax sum."""
+        import torch
+        if o is None:                    # rows that belong to no token are zero in a tensor made here
+            o = torch.zeros_like(q)
+        if o.shape != q.shape:
+            raise ValueError("o must have q's shape")
+        if lse is not None:
+            shape = q.shape[:-1]
+            if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous() or lse.device != self.device:
+                raise ValueError(f"lse must be a contiguous float32 tensor {tuple(shape)} on {self.device}")
+        self._call(C.pisa_cache_attention, (self.c, seqs.c, self.heads, bool(causal), int(window), softmax_scale,
+                                            self._rows(seqs, q, self.heads, "q"),
+                                            self._rows(seqs, o, self.heads, "o"), lse), stream)
+        return o
+
+    def device_error(self, stream=None):
+        return C.pisa_read_device_error(self.ws, stream)
+
+
 AXIS_ORDERS = ("thw", "twh", "htw", "hwt", "wth", "wht")
 
 
