@@ -1,0 +1,698 @@
+// Attention over the paged cache for few query rows a key/value head (single tokens, a handful of
+// tokens): bf16 and e4m3 pools.
+//
+// The new tokens of a sequence times the group of query heads that share a key/value head are the
+// rows (at most 64) of one small matrix product with that head's keys, so every stored key and value
+// is read from HBM once and serves all of them; the kernel is bound by that stream.
+//
+// Work: an item is (sequence, key/value head); its keys are cut into tiles of 64.  All items' tiles
+// form one line that is cut into equal shares, one a block, whatever the lengths: a block walks
+// through the end of one item, whole items, and the beginning of another.  Items that several
+// blocks share leave partial results (O, maximum, sum) in the workspace; the block that finishes
+// last joins them in the order of the blocks, so the result does not depend on which that is.
+//
+// Block: a producer warp that follows the page table and fills a ring of shared-memory stages with
+// TMA (a 128-byte-swizzled box a page), and 4 consumer warps.  With MT row tiles of 16 the warps are
+// MT row groups x 4 / MT key groups; each multiplies its rows with its own keys of a tile by
+// mma.m16n8k16 (rows are too few to fill a tcgen05 tile, and the tensor pipe has room: 64 keys of a
+// row tile take 128 mma), keeps its own running maximum and sum, and the key groups are joined at
+// the item's end through one stage of the ring.  O is rescaled only when a row's maximum grows by
+// more than 2^8 (weights stay finite, sums are fp32).
+//
+// e4m3 pools: codes become fp16 exactly (one instruction for two), q becomes fp16 with a power of
+// two per row, also exactly, and a key's scales act on the logits: with x_j = s_j + e_j (e_j the
+// exponent of v_j's scale, in base-2 logits) the weight of code row j is 2^(x_j - M), M the maximum of
+// the x, and the sum takes 2^(x_j - M) 2^-e_j.  So the fp16 weights keep 11 bits for what counts most
+// in O, however the rows' scales differ.
+//
+// Positions that a row does not see get weight zero; the V rows behind the last position (stale
+// slots) are zeroed in registers, because 0 * NaN is NaN, and a value that is not finite where only
+// some rows see it is taken out of the product and added to those rows alone.
+#include "cache.cuh"
+#include "sm100.cuh"
+
+namespace pisa {
+namespace cache {
+namespace {
+using namespace sm100;
+
+constexpr int kTile = 64;                    // keys
+constexpr int kConsumers = 128;
+constexpr int kThreads = kConsumers + 32;
+constexpr float kLazyLog2 = 8.f;
+constexpr unsigned FULL = 0xffffffffu;
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool kF16>
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (kF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int D, bool kF8>
+struct Layout {
+  static constexpr int kRowBytes = kF8 ? D : 128;                 // of a swizzled tile's row
+  static constexpr int kHalves = kF8 ? 1 : D / 64;                // 64-column bf16 halves
+  static constexpr int kSide = kTile * D * (kF8 ? 1 : 2);         // bytes of a K or V tile
+  static constexpr int kStages = kF8 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+};
+
+template <int D, bool kF8>
+struct alignas(1024) Smem {
+  using L = Layout<D, kF8>;
+  uint8_t k[L::kStages][L::kSide];
+  uint8_t v[L::kStages][L::kSide];
+  uint8_t ke[L::kStages][kF8 ? kTile : 16];
+  uint8_t ve[L::kStages][kF8 ? kTile : 16];
+  uint64_t full[L::kStages], empty[L::kStages];
+  unsigned long long bad[L::kStages];        // keys of the tile whose page is no page of the pool, or is not there
+  long long scan[kThreads / 32], before;
+  float2 ml[2][16];                          // maximum and sum of the rows that a warp hands over
+  int start_b, abort, last;
+};
+
+struct Params {
+  AttnArgs a;
+  int* counters;             // one a block, zero between calls
+  float2* part_ml;           // [2 * blocks][64]: maximum and sum of a partial result's rows
+  float* part_o;             // [2 * blocks][64][D]
+  int min_share;
+  unsigned long long wait_ns;
+};
+
+// An item's keys in tiles: tiles [t0, t0 + n) of the sequence, n = 0 for no new token.
+struct Item {
+  Seq s;
+  int t0, n;
+};
+__device__ __forceinline__ Item load_item(const AttnArgs& a, int b) {
+  Item it;
+  it.t0 = it.n = 0;
+  if (!load_seq(a.seqs, b, a.q.rows, &it.s) || it.s.n == 0) return it;
+  const int first = a.window > 0 ? max(0, min(it.s.len, it.s.len - it.s.n - a.window + 1)) : 0;
+  it.t0 = first / kTile;
+  it.n = max(1, (it.s.len + kTile - 1) / kTile - it.t0);      // an empty sequence's rows are written too
+  return it;
+}
+
+// Waits for a phase; after a timeout every wait returns at once and the block runs to its end on
+// whatever shared memory holds (the status word says so), so that no warp is left at a barrier.
+template <typename S>
+__device__ __forceinline__ void wait(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
+  if (!mbar_wait_bounded(bar, parity, &sm.abort, p.wait_ns)) {
+    *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+    set_status(p.a.seqs.status, PISA_DEVERR_WAIT_TIMEOUT);
+  }
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile as TMA wrote it.
+template <int D, bool kF8>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if (kF8) return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Element (row r, column c) of a V tile.
+template <int D, bool kF8>
+__device__ __forceinline__ float value_at(const uint8_t* tile, int r, int c) {
+  if (kF8) {
+    const uint32_t h = e4m3x2_to_f16x2(tile[chunk_at<D, true>(r, c >> 4) + (c & 15)]);
+    return __half2float(__ushort_as_half((unsigned short)h));
+  }
+  return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(tile + chunk_at<D, false>(r, c >> 3) + 2 * (c & 7)));
+}
+
+template <int D, bool kF8, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
+  using L = Layout<D, kF8>;
+  constexpr int kStages = L::kStages;
+  constexpr int kKeyGroups = 4 / MT, kSteps = 4 / kKeyGroups;     // 16-key steps of a warp in a tile
+  extern __shared__ uint8_t smem_raw[];
+  Smem<D, kF8>& sm = *reinterpret_cast<Smem<D, kF8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this block's share of the line of tiles ----
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 4);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  long long mine = 0;
+  for (int b = threadIdx.x; b < a.seqs.batch; b += kThreads) mine += (long long)load_item(a, b).n * a.pool.kv_heads;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(FULL, mine, d);
+  if (lane == 0) sm.scan[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += sm.scan[w];
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < p.min_share) share = p.min_share;
+  const long long u0 = share * blockIdx.x, u1 = min(total, u0 + share);
+  if (u0 >= u1) return;
+  // the sequence that tile u0 belongs to, and the tiles before it: warp 0 scans 32 sequences at a time
+  if (warp == 0) {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.seqs.batch; b0 += 32) {
+      const long long n = b0 + lane < a.seqs.batch ? (long long)load_item(a, b0 + lane).n * a.pool.kv_heads : 0;
+      long long run = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long up = __shfl_up_sync(FULL, run, d);
+        if (lane >= d) run += up;
+      }
+      const unsigned hit = __ballot_sync(FULL, base + run > u0);
+      if (hit) {
+        const int w = __ffs(hit) - 1;
+        if (lane == w) {
+          sm.start_b = b0 + w;
+          sm.before = base + run - n;
+        }
+        break;
+      }
+      base += __shfl_sync(FULL, run, 31);
+    }
+  }
+  __syncthreads();
+
+  int b = sm.start_b;
+  Item it = load_item(a, b);
+  int h = (int)((u0 - sm.before) / it.n);
+  long long item0 = sm.before + (long long)h * it.n;          // the item's first tile in the line
+  int ring = 0;                                               // stages used so far
+  const auto next_item = [&]() {
+    item0 += it.n;
+    if (++h == a.pool.kv_heads) {
+      h = 0;
+      do it = load_item(a, ++b); while (it.n == 0);           // u < total: there is one
+    }
+  };
+
+  if (warp == 4) {
+    // =============================== producer ===============================
+    if (lane == 0) {
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+    }
+    const int box = min(a.pool.page, kTile), pages = kTile / box;      // boxes of a tile
+    const int per = 2 * L::kHalves;                                    // copies of a box
+    const uint32_t box_bytes = 2u * box * D * (kF8 ? 1 : 2) + (kF8 ? 2u * box : 0u);
+    for (long long u = u0; u < u1;) {
+      const int t_begin = it.t0 + (int)(u - item0), t_end = it.t0 + (int)(min(u1, item0 + it.n) - item0);
+      for (int t = t_begin; t < t_end; ++t, ++ring) {
+        const int st = ring % kStages;
+        if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
+        // lane i < pages looks box i's page up
+        int row = -1;
+        const int pos = t * kTile + lane * box;
+        if (lane < pages && pos < it.s.len) {
+          const int pg = load_page(a.seqs, a.pool, b, pos);
+          if (pg >= 0) row = (pg * a.pool.kv_heads + h) * a.pool.page + (pos & (a.pool.page - 1));
+        }
+        const unsigned have = __ballot_sync(FULL, row >= 0);
+        unsigned long long bad = 0;
+        for (int i = 0; i < pages; ++i)
+          if (!((have >> i) & 1u)) bad |= (box == 64 ? ~0ull : ((1ull << box) - 1ull)) << (i * box);
+        if (lane == 0) {
+          sm.bad[st] = bad;
+          mbar_expect_tx(&sm.full[st], __popc(have) * box_bytes);
+        }
+        __syncwarp();
+        // copies (box, K or V, half) over the lanes
+        for (int c = lane; c < ((pages * per + 31) & ~31); c += 32) {
+          const int i = c / per, side = c % per & 1, half = c % per >> 1;
+          const int r = __shfl_sync(FULL, row, i < pages ? i : 0);
+          if (i < pages && r >= 0) {
+            uint8_t* dst = (side ? sm.v[st] : sm.k[st]) + half * (kTile * 128) + i * box * L::kRowBytes;
+            tma_load_3d(dst, side ? &vmap : &kmap, &sm.full[st], half * 64, r, 0);
+            if (kF8) bulk_load((side ? sm.ve[st] : sm.ke[st]) + i * box, (side ? a.pool.v_exp : a.pool.k_exp) + r, box, &sm.full[st]);
+          }
+        }
+      }
+      if (kKeyGroups > 1) {                                   // the stage that the key groups are joined through
+        const int st = ring % kStages;
+        if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
+        if (lane == 0) mbar_arrive(&sm.full[st]);
+        ++ring;
+      }
+      u = item0 + it.n;
+      if (u < u1) next_item();
+    }
+    // every copy lands before this block's shared memory is released
+    if (lane == 0)
+      for (int i = max(0, ring - kStages); i < ring; ++i) mbar_drain(&sm.full[i % kStages], (i / kStages) & 1, p.wait_ns);
+  } else {
+    // =============================== consumers ===============================
+    const int rt = warp % MT, kg = warp / MT;                 // row tile, key group
+    const int g = lane >> 2, q4 = lane & 3;
+    for (long long u = u0; u < u1;) {
+      const int t_begin = it.t0 + (int)(u - item0), t_end = it.t0 + (int)(min(u1, item0 + it.n) - item0);
+      const int rows = it.s.n * a.group;
+      // my two rows: r0 = 16 rt + g and r0 + 8; queries straight into the A fragments
+      const int r0 = rt * 16 + g;
+      uint32_t qa[D / 16][4];
+      float rs[2] = {a.scale_log2, a.scale_log2};             // raw score -> base-2 logit
+      int first[2], last[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + 8 * e;
+        first[e] = last[e] = 0;
+        const char* src = nullptr;
+        if (r < rows) {
+          const int i = r / a.group, hh = h * a.group + r - i * a.group;
+          visible(a, it.s.len, it.s.len - it.s.n + i, &first[e], &last[e]);
+          src = a.q.data + b * a.q.seq + (long long)(it.s.row0 + i) * a.q.row + (long long)hh * a.q.head;
+        }
+        if constexpr (kF8) {
+          // K fragments hold codes 4 q4 ... 4 q4 + 3 of a 16-code chunk as their k positions 2 q4, 2 q4 + 1 and +8
+          uint2 w[D / 16];
+          uint32_t m = 0;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            w[c] = src ? *reinterpret_cast<const uint2*>(src + c * 32 + q4 * 8) : make_uint2(0, 0);
+            m = max(m, max(max((w[c].x << 16) & 0x7fff0000u, w[c].x & 0x7fff0000u),
+                           max((w[c].y << 16) & 0x7fff0000u, w[c].y & 0x7fff0000u)));
+          }
+          m = max(m, __shfl_xor_sync(FULL, m, 1));
+          m = max(m, __shfl_xor_sync(FULL, m, 2));
+          // largest magnitude to [2^14, 2^15): every bf16 down to 2^-31 of it is an fp16 number
+          const int eq = max(-100, min(112, (int)(m >> 23) - 127 - 14));
+          const float s = pow2(-eq);
+          rs[e] *= pow2(eq);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            qa[c][e] = pack_f16x2(__uint_as_float(w[c].x << 16) * s, __uint_as_float(w[c].x & 0xffff0000u) * s);
+            qa[c][2 + e] = pack_f16x2(__uint_as_float(w[c].y << 16) * s, __uint_as_float(w[c].y & 0xffff0000u) * s);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            qa[c][e] = src ? *reinterpret_cast<const uint32_t*>(src + c * 32 + q4 * 4) : 0u;
+            qa[c][2 + e] = src ? *reinterpret_cast<const uint32_t*>(src + c * 32 + 16 + q4 * 4) : 0u;
+          }
+        }
+      }
+      // keys that all of the warp's rows see: only those tiles need no masks
+      int all_first = r0 < rows ? first[0] : 0, all_last = r0 < rows ? last[0] : 0x7fffffff;
+      if (r0 + 8 < rows) {
+        all_first = max(all_first, first[1]);
+        all_last = min(all_last, last[1]);
+      }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        all_first = max(all_first, __shfl_xor_sync(FULL, all_first, d));
+        all_last = min(all_last, __shfl_xor_sync(FULL, all_last, d));
+      }
+      all_last = min(all_last, it.s.len);
+      float acc[D / 8][4];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+      for (int t = t_begin; t < t_end; ++t, ++ring) {
+        const int st = ring % kStages;
+        wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+        const uint32_t kb = smem_u32(sm.k[st]), vb = smem_u32(sm.v[st]);
+        const unsigned long long bad = sm.bad[st];
+#pragma unroll 1
+        for (int step = 0; step < kSteps; ++step) {
+          const int k0 = (kg * kSteps + step) * 16, j0 = t * kTile + k0;    // 16 keys
+          const unsigned bad16 = (unsigned)(bad >> k0) & 0xffffu;
+          const bool edge = j0 < all_first || j0 + 16 > all_last || bad16;
+          // ---- scores of 16 rows x 16 keys ----
+          float s[2][4] = {};
+          if (kF8) {
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2) {
+              uint32_t x[4];
+              ldsm4(kb + chunk_at<D, true>(k0 + ((lane >> 3) & 1) * 8 + (lane & 7), c + (lane >> 4)), x);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                mma16816<true>(s[0], qa[c + e], e4m3x2_to_f16x2((uint16_t)x[2 * e]), e4m3x2_to_f16x2((uint16_t)(x[2 * e] >> 16)));
+                mma16816<true>(s[1], qa[c + e], e4m3x2_to_f16x2((uint16_t)x[2 * e + 1]), e4m3x2_to_f16x2((uint16_t)(x[2 * e + 1] >> 16)));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t x[4];
+              ldsm4(kb + chunk_at<D, false>(k0 + (lane >> 4) * 8 + (lane & 7), 2 * c + ((lane >> 3) & 1)), x);
+              mma16816<false>(s[0], qa[c], x[0], x[1]);
+              mma16816<false>(s[1], qa[c], x[2], x[3]);
+            }
+          }
+          // ---- base-2 logits; my keys are 8 n + 2 q4 + {0, 1} ----
+          float inv[2][2];                                    // e4m3: 2^-e of my keys' values
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (kF8) {
+              const int at = k0 + 8 * n + 2 * q4;
+              const uint32_t ke = *reinterpret_cast<const uint16_t*>(&sm.ke[st][at]);
+              const uint32_t ve = *reinterpret_cast<const uint16_t*>(&sm.ve[st][at]);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t kx = (ke >> (8 * x)) & 0xffu, vx = (ve >> (8 * x)) & 0xffu;
+                const float ks = __uint_as_float(kx << 23), ef = (float)((int)vx - kExpBias);
+                inv[n][x] = __uint_as_float((254u - vx) << 23);
+                s[n][x] = fmaf(s[n][x] * ks, rs[0], ef);
+                s[n][2 + x] = fmaf(s[n][2 + x] * ks, rs[1], ef);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) s[n][x] *= a.scale_log2;
+            }
+          }
+          unsigned seen = 0xffu;                              // bit 4 n + x
+          if (edge) {
+            seen = 0;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int kk = 8 * n + 2 * q4 + (x & 1), j = j0 + kk;
+                if (j >= first[x >> 1] && j < last[x >> 1] && !((bad16 >> kk) & 1u)) seen |= 1u << (4 * n + x);
+                else s[n][x] = -INFINITY;
+              }
+          }
+          // ---- running maximum: moved only when a row outgrows it by 2^8 ----
+          const float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+          const float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+          if (__any_sync(FULL, x0 > m[0] + kLazyLog2 || x1 > m[1] + kLazyLog2)) {
+            float mx[2] = {x0, x1}, f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(FULL, mx[e], 1));
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(FULL, mx[e], 2));
+              const float mn = fmaxf(m[e], mx[e]);
+              f[e] = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
+              m[e] = mn;
+              l[e] *= f[e];
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              acc[c][0] *= f[0];
+              acc[c][1] *= f[0];
+              acc[c][2] *= f[1];
+              acc[c][3] *= f[1];
+            }
+          }
+          const float mb[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+          float w[2][4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              w[n][x] = ex2(s[n][x] - mb[x >> 1]);
+              if (kF8) {
+                if (!edge || ((seen >> (4 * n + x)) & 1u)) l[x >> 1] = fmaf(w[n][x], inv[n][x & 1], l[x >> 1]);
+              } else {
+                l[x >> 1] += w[n][x];
+              }
+            }
+          uint32_t pa[4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              pa[2 * n + e] = kF8 ? pack_f16x2(w[n][2 * e], w[n][2 * e + 1]) : pack_bf16x2(w[n][2 * e], w[n][2 * e + 1]);
+          // ---- O += P V ----
+          uint32_t keep[2] = {FULL, FULL};                    // edge: my V rows (keys 2 q4, +1, and +8) that exist
+          if (edge) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              keep[n] = 0;
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int kk = 8 * n + 2 * q4 + x;
+                if (j0 + kk < it.s.len && !((bad16 >> kk) & 1u)) keep[n] |= 0xffffu << (16 * x);
+              }
+            }
+          }
+          constexpr uint32_t kInf = kF8 ? 0x7c007c00u : 0x7f807f80u;
+          bool odd = false;                                   // a value that is not finite where not all rows see it
+          const auto clean = [&](uint32_t x, int n) -> uint32_t {
+            if (!edge) return x;
+            x &= keep[n];
+            const bool lo = (x & kInf & 0xffffu) == (kInf & 0xffffu), hi = (x & kInf & 0xffff0000u) == (kInf & 0xffff0000u);
+            odd = odd || lo || hi;
+            if (lo) x &= 0xffff0000u;
+            if (hi) x &= 0x0000ffffu;
+            return x;
+          };
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t x[4];
+            if constexpr (kF8) {
+              if (c & 1) continue;
+              ldsm4t(vb + chunk_at<D, true>(k0 + ((lane >> 3) & 1) * 8 + (lane & 7), c + (lane >> 4)), x);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // bytes (key, d), (key, d + 1), (key + 1, d), (key + 1, d + 1) -> pairs of keys for d and for d + 1
+                const uint32_t lo = __byte_perm(x[2 * e], 0, 0x3120), hi = __byte_perm(x[2 * e + 1], 0, 0x3120);
+                mma16816<true>(acc[2 * (c + e)], pa, clean(e4m3x2_to_f16x2((uint16_t)lo), 0), clean(e4m3x2_to_f16x2((uint16_t)hi), 1));
+                mma16816<true>(acc[2 * (c + e) + 1], pa, clean(e4m3x2_to_f16x2((uint16_t)(lo >> 16)), 0),
+                               clean(e4m3x2_to_f16x2((uint16_t)(hi >> 16)), 1));
+              }
+            } else {
+              ldsm4t(vb + chunk_at<D, false>(k0 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * c + (lane >> 4)), x);
+              mma16816<false>(acc[2 * c], pa, clean(x[0], 0), clean(x[1], 1));
+              mma16816<false>(acc[2 * c + 1], pa, clean(x[2], 0), clean(x[3], 1));
+            }
+          }
+          if (edge && __any_sync(FULL, odd)) {
+            // rare: add what was taken out, to the rows that see it
+#pragma unroll 1
+            for (int kk = 0; kk < 16; ++kk) {
+              if (j0 + kk >= it.s.len || ((bad16 >> kk) & 1u)) continue;
+              const int src = (lane & ~3) | ((kk & 7) >> 1);
+              const int n = kk >> 3, x = kk & 1;
+              float wk[2];
+              bool sk[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float mine_w = n ? (x ? w[1][2 * e + 1] : w[1][2 * e]) : (x ? w[0][2 * e + 1] : w[0][2 * e]);
+                wk[e] = __shfl_sync(FULL, mine_w, src);
+                sk[e] = (__shfl_sync(FULL, seen, src) >> (4 * n + 2 * e + x)) & 1u;
+              }
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int col = kF8 ? 16 * (c >> 1) + 4 * q4 + 2 * y + (c & 1) : 8 * c + 2 * q4 + y;
+                  const float val = value_at<D, kF8>(sm.v[st], k0 + kk, col);
+                  if (isfinite(val)) continue;
+                  if (sk[0]) acc[c][y] = fmaf(wk[0], val, acc[c][y]);
+                  if (sk[1]) acc[c][2 + y] = fmaf(wk[1], val, acc[c][2 + y]);
+                }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[st]);
+      }
+      // ---- the row sums of the four lanes of a row, then the key groups ----
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(FULL, l[e], 1);
+        l[e] += __shfl_xor_sync(FULL, l[e], 2);
+      }
+      if (kKeyGroups > 1) {
+        const int st = ring % kStages;
+        wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+        // one side of the stage takes the O of one warp, element by element a lane; at most two give at a time
+        static_assert(L::kSide >= 16 * D * 4, "");
+#pragma unroll
+        for (int from = kKeyGroups / 2; from > 0; from >>= 1) {
+          const int pair = (kg % from) * MT + rt;              // groups [from, 2 from) give theirs to [0, from)
+          float* buf = reinterpret_cast<float*>(pair ? sm.v[st] : sm.k[st]) + lane;
+          if (kg >= from && kg < 2 * from) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) buf[(4 * c + x) * 32] = acc[c][x];
+            if (q4 == 0) {
+              sm.ml[pair][g] = make_float2(m[0], l[0]);
+              sm.ml[pair][g + 8] = make_float2(m[1], l[1]);
+            }
+          }
+          consumer_sync();
+          if (kg < from) {
+            float f[2], fo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 o = sm.ml[pair][g + 8 * e];
+              const float mn = fmaxf(m[e], o.x), base = mn == -INFINITY ? 0.f : mn;
+              f[e] = ex2(m[e] - base);
+              fo[e] = ex2(o.x - base);
+              m[e] = mn;
+              l[e] = l[e] * f[e] + o.y * fo[e];
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[c][x] = acc[c][x] * f[x >> 1] + buf[(4 * c + x) * 32] * fo[x >> 1];
+          }
+          consumer_sync();
+        }
+        fence_async_shared();                                  // the stage goes back to TMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[st]);
+        ++ring;
+      }
+
+      // ---- the rows' results: complete, or a part of an item that other blocks work on too ----
+      const int c0 = (int)(item0 / share), c1 = (int)((item0 + it.n - 1) / share);
+      if (kg == 0) {
+        const int slot = 2 * blockIdx.x + (item0 < u0 ? 0 : 1);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 8 * e;
+          if (r >= rows) continue;
+          if (c0 == c1) {
+            const int i = r / a.group, hh = h * a.group + r - i * a.group;
+            char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
+            const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const float x = acc[c][2 * e] * inv, y = acc[c][2 * e + 1] * inv;
+              if constexpr (kF8) {
+                if (c & 1) continue;
+                const float x1 = acc[c + 1][2 * e] * inv, y1 = acc[c + 1][2 * e + 1] * inv;
+                *reinterpret_cast<uint2*>(dst + (8 * c + 4 * q4) * 2) = make_uint2(pack_bf16x2(x, x1), pack_bf16x2(y, y1));
+              } else {
+                *reinterpret_cast<uint32_t*>(dst + (8 * c + 2 * q4) * 2) = pack_bf16x2(x, y);
+              }
+            }
+            float* lse = lse_at(a, b, it.s, i, hh);
+            if (lse && q4 == 0) *lse = l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * 0.6931471805599453f;
+          } else {
+            float* dst = p.part_o + ((size_t)slot * kMaxFewRows + r) * D;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              if constexpr (kF8) {
+                if (c & 1) continue;
+                *reinterpret_cast<float4*>(dst + 8 * c + 4 * q4) =
+                    make_float4(acc[c][2 * e], acc[c + 1][2 * e], acc[c][2 * e + 1], acc[c + 1][2 * e + 1]);
+              } else {
+                *reinterpret_cast<float2*>(dst + 8 * c + 2 * q4) = make_float2(acc[c][2 * e], acc[c][2 * e + 1]);
+              }
+            }
+            if (q4 == 0) p.part_ml[(size_t)slot * kMaxFewRows + r] = make_float2(m[e], l[e]);
+          }
+        }
+      }
+      if (c0 != c1) {
+        __threadfence();
+        consumer_sync();
+        if (threadIdx.x == 0) {
+          const bool done = atomicAdd(p.counters + c0, 1) == c1 - c0;
+          if (done) p.counters[c0] = 0;                        // as the next call finds it
+          sm.last = done;
+        }
+        consumer_sync();
+        if (sm.last) {
+          __threadfence();
+          constexpr int kLanes = D / 4;                        // threads a row, four columns each
+          for (int r = threadIdx.x / kLanes; r < rows; r += kConsumers / kLanes) {
+            const int col = (threadIdx.x % kLanes) * 4;
+            float mm = -INFINITY;
+            for (int c = c0; c <= c1; ++c)
+              mm = fmaxf(mm, __ldcg(&p.part_ml[(size_t)(2 * c + (c == c0)) * kMaxFewRows + r]).x);
+            const float base = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const size_t at = (size_t)(2 * c + (c == c0)) * kMaxFewRows + r;
+              const float2 ml = __ldcg(&p.part_ml[at]);
+              const float4 po = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + col));
+              const float f = ex2(ml.x - base);
+              ll = fmaf(ml.y, f, ll);
+              o.x = fmaf(po.x, f, o.x);
+              o.y = fmaf(po.y, f, o.y);
+              o.z = fmaf(po.z, f, o.z);
+              o.w = fmaf(po.w, f, o.w);
+            }
+            const int i = r / a.group, hh = h * a.group + r - i * a.group;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
+            *reinterpret_cast<uint2*>(dst + col * 2) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            float* lse = lse_at(a, b, it.s, i, hh);
+            if (lse && col == 0) *lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+          }
+        }
+      }
+      u = item0 + it.n;
+      if (u < u1) next_item();
+    }
+  }
+}
+
+template <int D, bool kF8, int MT>
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const size_t smem = sizeof(Smem<D, kF8>) + 1024;
+  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_few<D, kF8, MT>), smem))) return e;
+  // no more blocks than there can be tiles
+  const long long tiles = (long long)p.a.seqs.batch * p.a.pool.kv_heads * ((p.a.seqs.max_len + kTile - 1) / kTile + 1);
+  const int blocks = (int)min((long long)min(2 * sms, kMaxFewBlocks), tiles);
+  attn_few<D, kF8, MT><<<blocks, kThreads, smem, st>>>(km, vm, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool kF8>
+cudaError_t launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Params& p, cudaStream_t st) {
+  const long long rows = (long long)p.a.seqs.max_new * p.a.group;
+  if (rows <= 16) return launch<D, kF8, 1>(km, vm, p, st);
+  if (rows <= 32) return launch<D, kF8, 2>(km, vm, p, st);
+  return launch<D, kF8, 4>(km, vm, p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned long long wait_ns, cudaStream_t st) {
+  CUtensorMap km, vm;
+  const uint64_t rows = (uint64_t)a.pool.num_pages * a.pool.kv_heads * a.pool.page;
+  const int esz = a.pool.dtype == PISA_CACHE_E4M3 ? 1 : 2;
+  const uint32_t box = a.pool.page < kTile ? a.pool.page : kTile;
+  if (!encode_rows(&km, a.pool.k, esz, d, rows, box) || !encode_rows(&vm, a.pool.v, esz, d, rows, box))
+    return cudaErrorInvalidValue;
+  Params p;
+  p.a = a;
+  char* w = static_cast<char*>(ws);
+  p.counters = reinterpret_cast<int*>(w + kCountersAt);
+  p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
+  p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxFewBlocks * kMaxFewRows);
+  p.min_share = 2;
+  p.wait_ns = wait_ns;
+  if (esz == 1) return d == 64 ? launch_rows<64, true>(km, vm, p, st) : launch_rows<128, true>(km, vm, p, st);
+  return d == 64 ? launch_rows<64, false>(km, vm, p, st) : launch_rows<128, false>(km, vm, p, st);
+}
+
+}  // namespace cache
+}  // namespace pisa

@@ -82,6 +82,11 @@ bool encode_16bit_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_
 bool encode_u8_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t batch,
                   uint32_t box_rows);
 
+// Rows of `inner` (64 or 128) bf16 (elem_bytes 2) or e4m3 (1) numbers, one after another, with a box of
+// box_rows rows: 64 columns of bf16 or whole e4m3 rows, 128 bytes wide and swizzled over 128 bytes
+// (64-byte e4m3 rows: over 64).
+bool encode_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows, uint32_t box_rows);
+
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // bounded mbarrier waits: 2 s
 
 // cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) on the current

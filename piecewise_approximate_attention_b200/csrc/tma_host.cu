@@ -115,4 +115,18 @@ bool encode_u8_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t r
   return r == CUDA_SUCCESS;
 }
 
+bool encode_rows(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+  if (elem_bytes == 2) return encode_16bit_3d(map, base, inner, rows, 1, box_rows, false);
+  auto fn = encode_fn();
+  if (!fn || !base) return false;
+  cuuint64_t dims[3] = {inner, rows, 1};
+  cuuint64_t strides[2] = {inner, rows * inner};
+  cuuint32_t box[3] = {(cuuint32_t)inner, box_rows, 1};
+  cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estride,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace pisa
