@@ -32,7 +32,7 @@ extern "C" {
  *
  * PISA_CACHE_E4M3 stores each token's head as head_dim e4m3 codes and one biased exponent byte:
  *     value = code * 2^(exp - 127),  exp - 127 = the smallest e with max|x| <= 448 * 2^e, kept in
- *     [-50, 50] (0 for a row of zeros); code = e4m3(x * 2^-e), to nearest even, saturated.
+ *     [-50, 50]; code = e4m3(x * 2^-e), to nearest even, saturated.
  * A power of two keeps every stored value a bf16 number (reading back is exact) and lets the
  * attention kernels carry it in the exponents of the softmax weights; the limit of 50 is what their
  * fp32 sums can take.  Rows above 448 * 2^50 saturate, an infinity is stored as the largest code,
@@ -64,7 +64,8 @@ typedef struct {
   int32_t max_pages;           /* row length of page_table */
   int32_t max_len;             /* >= every lens[b]; <= max_pages * page */
   int32_t max_new;             /* >= every n_b */
-  const int32_t* page_table;   /* [batch, max_pages]; only the first ceil(lens[b] / page) of a row are read */
+  const int32_t* page_table;   /* [batch, max_pages]; of a row only the first ceil(lens[b] / page) are read, and
+                                * none whose tokens all lie before what a windowed attention sees */
   const int32_t* lens;         /* [batch] tokens of each sequence, the new ones included */
   const int32_t* starts;       /* nullable [batch + 1] */
   const int32_t* counts;       /* nullable [batch] */

@@ -126,7 +126,11 @@ __device__ __forceinline__ float* lse_at(const AttnArgs& a, int b, const Seq& s,
 constexpr int kMaxFewBlocks = 296, kMaxFewRows = 64;       // few-row attention: two blocks on each of 148 SMs
 constexpr size_t kCountersAt = kStatusBytes;
 constexpr size_t kPartialsAt = kCountersAt + (kMaxFewBlocks * sizeof(int) + 255) / 256 * 256;
-inline size_t few_partials_bytes(int d) { return (size_t)2 * kMaxFewBlocks * kMaxFewRows * (d + 2) * sizeof(float); }
+constexpr int kMaxChunkBlocks = 148, kMaxChunkRows = 256;  // chunk attention: one block an SM
+inline size_t partials_bytes(int d) {
+  const size_t few = (size_t)kMaxFewBlocks * kMaxFewRows, chunk = (size_t)kMaxChunkBlocks * kMaxChunkRows;
+  return 2 * (few > chunk ? few : chunk) * (d + 2) * sizeof(float);
+}
 
 // ---- launchers ----
 cudaError_t launch_append(const Pool& pool, int head_dim, const Seqs& seqs, const Rows& k, const Rows& v, cudaStream_t st);
@@ -134,6 +138,8 @@ cudaError_t launch_read(const Pool& pool, int head_dim, const Seqs& seqs, const 
 cudaError_t launch_attention_simt(const AttnArgs& a, int head_dim, cudaStream_t st);
 // bf16 and e4m3 pools, at most kMaxFewRows rows (new tokens times query heads of a key/value head).
 cudaError_t launch_attention_few(const AttnArgs& a, int head_dim, void* ws, unsigned long long wait_ns, cudaStream_t st);
+// bf16 and e4m3 pools, any number of rows.
+cudaError_t launch_attention_chunk(const AttnArgs& a, int head_dim, void* ws, unsigned long long wait_ns, cudaStream_t st);
 
 }  // namespace cache
 }  // namespace pisa

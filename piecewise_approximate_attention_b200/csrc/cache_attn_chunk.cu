@@ -1,0 +1,799 @@
+// Attention over the paged cache for chunks of new tokens: bf16 and e4m3 pools, TMA + tcgen05.
+//
+// The new tokens of a sequence times the group of query heads that share a key/value head are the
+// rows of one product with that head's keys.  An item is up to 256 of these rows: two tiles ("slots")
+// of 128 that walk the same tiles of 128 keys together, so a key tile is read from L2 once for 256
+// rows, and one slot's softmax runs while the tensor core works on the other's products.  As in the
+// few-row kernel all items' key tiles form one line that is cut into equal shares, one a block, and
+// items that several blocks share are joined through the workspace by the block that ends last.
+//
+// Block (one an SM, 16 warps):
+//   warps 0-3, 4-7   softmax and output of slot 0 and 1: thread r owns row r (TMEM lane r).  Per tile
+//                    and half of 64 keys: scores from TMEM, running maximum (moved only when a row
+//                    outgrows it by 2^8), P back over the scores' columns, release to the MMA warp
+//   warps 8-11       values made ready: see below; thread r owns key r of the tile
+//   warp 12          follows the page table, TMA loads into two K and two V stages
+//   warp 13          issues the MMAs: S = Q K^T (M 128, N 128), O += P V per half (P from TMEM)
+// TMEM: S/P of the slots at columns 0 and 128, O at 256 and 384.
+//
+// bf16 pools: K and V are used as stored; P is bf16, as the type of V asks of the MMA (each weight is
+// off by 2^-8 at most, like the output's own rounding).
+// e4m3 pools: warps 8-11 turn codes into fp16 tiles in shared memory, once for both slots, as
+// code * 2^(e - E): e the row's own exponent, E the largest of the share's first tile.  That is exact
+// for e - E in [-15, 7], so scores need one factor 2^E a share and P (fp16, 11 bits) multiplies values
+// that are all in one unit.  q becomes fp16 with a power of two per row, exactly.
+//
+// What does not fit is computed again: a share in which a row's exponent leaves that window, or that
+// holds a value which is not finite in a tile that only some rows see (0 * NaN would reach the rows
+// that do not), is flagged and its rows are computed by the plain routine of cache_row.cuh.  V rows of
+// stale slots and of missing pages are zeroed.
+#include "cache_row.cuh"
+#include "sm100.cuh"
+
+namespace pisa {
+namespace cache {
+namespace {
+using namespace sm100;
+
+constexpr int kKeys = 128;                   // keys of a tile
+constexpr int kRows = 128;                   // rows of a slot
+constexpr int kThreads = 512;
+constexpr int kSoftmax = 256;
+constexpr float kLazyLog2 = 8.f;
+constexpr unsigned FULL = 0xffffffffu;
+constexpr uint32_t kColO = 256;
+constexpr int kStages = 2;
+constexpr int kBelow = 15, kAbove = 7;       // exponents that fp16 holds exactly around E
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+template <int D, bool kF8>
+struct alignas(1024) Smem {
+  static constexpr int kHalf = kKeys * 128;              // 128 rows of 64 16-bit columns
+  static constexpr int kTile = D / 64 * kHalf;
+  uint8_t q[2][kTile];
+  uint8_t k[kStages][kTile];
+  uint8_t v[kStages][kTile];
+  uint8_t raw[kF8 ? 2 : 1][kF8 ? kKeys * D : 16];        // e4m3 codes as loaded, K and V in turn
+  uint8_t raw_exp[2][kKeys];
+  float row_scale[kF8 ? 2 * kRows : 1];                  // raw score -> base-2 logit, but for 2^E
+  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], vready[kStages];
+  uint64_t rawfull[2], rawempty[2];
+  uint64_t qfull[2], sfull[2], pfull[2][2], odone[2][2], drain;
+  uint32_t bad[4][4];                                    // tile of the block & 3: keys whose page is missing
+  int unit[4][2], odd[4];                                // item & 3: E of K and V; to be computed again
+  int red[4];
+  long long scan[kThreads / 32], before;
+  uint32_t tmem;
+  int abort, last, start_b, start_h, start_p;
+};
+
+struct Params {
+  AttnArgs a;
+  int* counters;             // one a block, zero between calls
+  float2* part_ml;           // [2 * blocks][256]
+  float* part_o;             // [2 * blocks][256][D]
+  int item_cost;
+  unsigned long long wait_ns;
+};
+
+// Rows [256 p, 256 p + rows) of a sequence and key/value head; their keys are tiles [t0, t0 + n).
+struct Item {
+  int t0, n, rows, first;             // first: the first key that any row sees
+  long long cost;
+};
+__device__ __forceinline__ int pairs_of(const AttnArgs& a, const Seq& s) { return (s.n * a.group + 255) / 256; }
+__device__ __forceinline__ Item item_of(const AttnArgs& a, const Seq& s, int p, int item_cost) {
+  Item it;
+  it.rows = min(256, s.n * a.group - 256 * p);
+  int f0, l0, f1, l1;
+  const int pos = s.len - s.n;
+  visible(a, s.len, pos + 256 * p / a.group, &f0, &l0);
+  visible(a, s.len, pos + (256 * p + it.rows - 1) / a.group, &f1, &l1);
+  // rows that see nothing (before the cache's first position) leave the range to the others
+  const int first = l0 > f0 ? f0 : 0, last = max(l0, l1);
+  it.first = first;
+  it.t0 = first / kKeys;
+  it.n = max(1, (last + kKeys - 1) / kKeys - it.t0);
+  it.cost = it.n + item_cost;
+  return it;
+}
+
+// After a timeout every wait returns at once and the block runs to its end on whatever its memory
+// holds (the status word says so), so that no warp is left at a barrier.
+template <typename S>
+__device__ __forceinline__ void wait(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
+  if (!mbar_wait_bounded(bar, parity, &sm.abort, p.wait_ns)) {
+    *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+    set_status(p.a.seqs.status, PISA_DEVERR_WAIT_TIMEOUT);
+  }
+}
+
+// Bits of 32 keys from j0 on that lie in [first, last).
+__device__ __forceinline__ uint32_t range_bits(int j0, int first, int last) {
+  const int lo = first - j0, hi = last - j0;
+  uint32_t m = hi >= 32 ? FULL : hi > 0 ? (1u << hi) - 1u : 0u;
+  if (lo > 0) m &= lo >= 32 ? 0u : ~((1u << lo) - 1u);
+  return m;
+}
+
+// Where a block is in the line of tiles; every role walks its own copy.
+struct Walk {
+  int b, h, p, pairs, count;          // count: items so far
+  Seq s;
+  Item it;
+  long long item0;
+  int t_begin, t_end;                 // this block's tiles of the item
+};
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
+  using S = Smem<D, kF8>;
+  extern __shared__ uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- set-up, and this block's share of the line ----
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.kfull[i], kF8 ? 4 : 1);
+      mbar_init(&sm.kempty[i], 1);
+      mbar_init(&sm.vfull[i], 1);
+      mbar_init(&sm.vempty[i], 1);
+      mbar_init(&sm.vready[i], 4);
+      mbar_init(&sm.rawfull[i], 1);
+      mbar_init(&sm.rawempty[i], 4);
+      mbar_init(&sm.qfull[i], kRows);
+      mbar_init(&sm.sfull[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm.pfull[i][h], kRows);
+        mbar_init(&sm.odone[i][h], 1);
+      }
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  // cost of a sequence and head: a warp a sequence, lanes over its row pairs
+  const auto seq_cost = [&](int b) -> long long {
+    Seq s;
+    long long c = 0;
+    if (b < a.seqs.batch && load_seq(a.seqs, b, a.q.rows, &s))
+      for (int i = lane; i < pairs_of(a, s); i += 32) c += item_of(a, s, i, p.item_cost).cost;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(FULL, c, d);
+    return c;
+  };
+  long long mine = 0;
+  for (int b = warp; b < a.seqs.batch; b += kThreads / 32) mine += seq_cost(b);
+  if (lane == 0) sm.scan[warp] = mine;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += sm.scan[w];
+  total *= a.pool.kv_heads;
+  const long long share = max(1LL + p.item_cost, (total + gridDim.x - 1) / gridDim.x);
+  const long long u0 = share * blockIdx.x, u1 = min(total, u0 + share);
+  if (u0 < u1) {
+    __syncthreads();                     // scan is used again
+    // the sequence of place u0: chunks of 16 sequences, one a warp
+    long long base = 0;
+    for (int b0 = 0; b0 < a.seqs.batch; b0 += kThreads / 32) {
+      const long long c = seq_cost(b0 + warp) * a.pool.kv_heads;
+      if (lane == 0) sm.scan[warp] = c;
+      __syncthreads();
+      long long run = base;
+      int found = -1;
+      for (int w = 0; w < kThreads / 32 && found < 0; ++w) {
+        if (u0 < run + sm.scan[w]) found = w;
+        else run += sm.scan[w];
+      }
+      if (found >= 0) {
+        if (warp == found) {             // the head, then the pair of rows, in it
+          Seq s;
+          load_seq(a.seqs, b0 + warp, a.q.rows, &s);
+          const long long per = c / a.pool.kv_heads;
+          const int h = (int)((u0 - run) / per);
+          run += h * per;
+          for (int i0 = 0;; i0 += 32) {
+            const long long n = i0 + lane < pairs_of(a, s) ? item_of(a, s, i0 + lane, p.item_cost).cost : 0;
+            long long upto = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const long long up = __shfl_up_sync(FULL, upto, d);
+              if (lane >= d) upto += up;
+            }
+            const unsigned hit = __ballot_sync(FULL, run + upto > u0);
+            if (hit || i0 + 32 >= pairs_of(a, s)) {
+              if (lane == (hit ? __ffs(hit) - 1 : 0)) {
+                sm.start_b = b0 + warp;
+                sm.start_h = h;
+                sm.start_p = i0 + lane;
+                sm.before = run + upto - n;
+              }
+              break;
+            }
+            run += __shfl_sync(FULL, upto, 31);
+          }
+        }
+        break;
+      }
+      base = run;
+      __syncthreads();
+    }
+    __syncthreads();
+
+    Walk w;
+    const auto enter = [&]() {
+      w.it = item_of(a, w.s, w.p, p.item_cost);
+      w.t_begin = w.it.t0 + (int)min((long long)w.it.n, max(0LL, u0 - w.item0));
+      w.t_end = w.it.t0 + (int)min((long long)w.it.n, u1 - w.item0);
+    };
+    w.b = sm.start_b;
+    w.h = sm.start_h;
+    w.p = sm.start_p;
+    w.item0 = sm.before;
+    w.count = 0;
+    load_seq(a.seqs, w.b, a.q.rows, &w.s);
+    w.pairs = pairs_of(a, w.s);
+    enter();
+    // the next item of this block, false at its share's end
+    const auto next = [&]() -> bool {
+      w.item0 += w.it.cost;
+      if (w.item0 >= u1) return false;
+      if (++w.p == w.pairs) {
+        w.p = 0;
+        if (++w.h == a.pool.kv_heads) {
+          w.h = 0;
+          do {
+            if (!load_seq(a.seqs, ++w.b, a.q.rows, &w.s)) w.s.n = 0;
+            w.pairs = pairs_of(a, w.s);
+          } while (w.pairs == 0);        // the line goes on: there is one
+        }
+      }
+      enter();
+      return true;
+    };
+
+    if (warp < 8) {
+      // =========================== softmax and output ===========================
+      const int slot = warp >> 2, r = threadIdx.x & (kRows - 1);
+      const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16), ts = trow + 128 * slot, to = trow + kColO + 128 * slot;
+      uint32_t n_tile = 0, all_tiles = 0;          // this slot's tiles so far, the block's
+      do {
+        if (w.t_begin >= w.t_end) continue;
+        const uint32_t tile0 = all_tiles;
+        all_tiles += w.t_end - w.t_begin;
+        const bool active = slot * kRows < w.it.rows;
+        const int row = slot * kRows + r, grow_ = 256 * w.p + row;          // of the item, of the head's rows
+        const bool valid = row < w.it.rows;
+        const int tok = valid ? grow_ / a.group : 0, head = w.h * a.group + (valid ? grow_ - tok * a.group : 0);
+        float m = -INFINITY, l = 0.f;
+        int first = 0, last = w.s.len;
+        if (valid) visible(a, w.s.len, w.s.len - w.s.n + tok, &first, &last);
+        if (active) {
+          // ---- the slot's queries into shared memory: each warp its own 32 rows, D / 8 lanes a row ----
+          constexpr int kLanes = D / 8;
+#pragma unroll 4
+          for (int rr = lane / kLanes; rr < 32; rr += 32 / kLanes) {
+            const int qr = (warp & 3) * 32 + rr, c = lane % kLanes, gr = 256 * w.p + slot * kRows + qr;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (slot * kRows + qr < w.it.rows) {
+              const int i = gr / a.group, hh = w.h * a.group + gr - i * a.group;
+              u = *reinterpret_cast<const uint4*>(a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row +
+                                                  (long long)hh * a.q.head + c * 16);
+            }
+            if constexpr (kF8) {
+              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+              uint32_t mx = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx = max(mx, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
+#pragma unroll
+              for (int d = kLanes / 2; d > 0; d >>= 1) mx = max(mx, __shfl_xor_sync(FULL, mx, d));
+              // largest magnitude to [2^14, 2^15): every bf16 down to 2^-31 of it is an fp16 number
+              const int eq = max(-100, min(112, (int)(mx >> 23) - 127 - 14));
+              const float sc = pow2(-eq);
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[e] = pack_f16x2(__uint_as_float(x[e] << 16) * sc, __uint_as_float(x[e] & 0xffff0000u) * sc);
+              u = make_uint4(y[0], y[1], y[2], y[3]);
+              if (c == 0) sm.row_scale[slot * kRows + qr] = a.scale_log2 * pow2(eq);
+            }
+            *reinterpret_cast<uint4*>(sm.q[slot] + (c >> 3) * S::kHalf + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = u;
+          }
+          fence_async_shared();
+          mbar_arrive(&sm.qfull[slot]);
+          __syncwarp();
+          // keys that all of the warp's rows see
+          int all_first = first, all_last = last;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) {
+            all_first = max(all_first, __shfl_xor_sync(FULL, all_first, d));
+            all_last = min(all_last, __shfl_xor_sync(FULL, all_last, d));
+          }
+          float sl = a.scale_log2;       // raw score -> base-2 logit
+          for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
+            const uint32_t par = n_tile & 1;
+            wait(sm, &sm.sfull[slot], par, p);
+            __syncwarp();
+            tc_fence_after();
+            if (kF8 && t == w.t_begin) sl = sm.row_scale[row] * pow2(sm.unit[w.count & 3][0]);
+            const uint32_t* bad = sm.bad[(tile0 + t - w.t_begin) & 3];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const int j0 = t * kKeys + 64 * hh;
+              uint32_t vm0 = FULL, vm1 = FULL;
+              if (j0 < all_first || j0 + 64 > all_last || (bad[2 * hh] | bad[2 * hh + 1])) {
+                vm0 = range_bits(j0, first, last) & ~bad[2 * hh];
+                vm1 = range_bits(j0 + 32, first, last) & ~bad[2 * hh + 1];
+                if (__all_sync(FULL, (vm0 | vm1) == 0u)) {
+                  // nothing to see for any of the warp's rows: P = 0, and m and l stay
+                  uint32_t zero[16];
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) zero[x] = 0u;
+                  tmem_st16(ts + 64 * hh, zero);
+                  tmem_st16(ts + 64 * hh + 16, zero);
+                  tmem_st_wait();
+                  tc_fence_before();
+                  mbar_arrive(&sm.pfull[slot][hh]);
+                  continue;
+                }
+              }
+              float s[64];
+              tmem_ld32(ts + 64 * hh, s);
+              tmem_ld32(ts + 64 * hh + 32, s + 32);
+              tmem_ld_wait();
+              if (vm0 != FULL) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] = ((vm0 >> x) & 1u) ? s[x] : -INFINITY;
+              }
+              if (vm1 != FULL) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[32 + x] = ((vm1 >> x) & 1u) ? s[32 + x] : -INFINITY;
+              }
+              float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]), t2 = fmaxf(s[4], s[5]), t3 = fmaxf(s[6], s[7]);
+#pragma unroll
+              for (int c = 8; c < 64; c += 8) {
+                t0 = fmax3(t0, s[c], s[c + 1]);
+                t1 = fmax3(t1, s[c + 2], s[c + 3]);
+                t2 = fmax3(t2, s[c + 4], s[c + 5]);
+                t3 = fmax3(t3, s[c + 6], s[c + 7]);
+              }
+              const float m_new = fmaxf(m, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sl);      // base-2 units
+              const bool grow = m_new > m + kLazyLog2;
+              const float f = grow ? ex2(m - m_new) : 1.f;     // 0 when m = -inf
+              if (grow) {
+                l *= f;
+                m = m_new;
+              }
+              const float mb = m == -INFINITY ? 0.f : m;
+              const uint64_t sc2 = f2_pack(sl, sl), nmb2 = f2_pack(-mb, -mb);
+              uint64_t acc2 = f2_pack(0.f, 0.f);
+#pragma unroll
+              for (int ch = 0; ch < 2; ++ch) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                  const int c = 32 * ch + x;
+                  float x0, x1;
+                  f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nmb2), x0, x1);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  acc2 = f2_add(acc2, f2_pack(p0, p1));
+                  pk[x >> 1] = kF8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                }
+                tmem_st16(ts + 64 * hh + 16 * ch, pk);
+              }
+              float ls0, ls1;
+              f2_unpack(acc2, ls0, ls1);
+              l += ls0 + ls1;
+              // O holds the products of the halves before this one: it is scaled before this half's P is released
+              if (__any_sync(FULL, grow) && (t > w.t_begin || hh > 0)) {
+                wait(sm, &sm.odone[slot][hh ^ 1], hh ? par : par ^ 1u, p);
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll
+                for (int ch = 0; ch < D / 32; ++ch) {
+                  float ov[32];
+                  tmem_ld32(to + 32 * ch, ov);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) ov[x] *= f;
+                  tmem_st32(to + 32 * ch, ov);
+                }
+              }
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&sm.pfull[slot][hh]);
+            }
+          }
+          wait(sm, &sm.odone[slot][1], (n_tile - 1) & 1, p);
+          __syncwarp();
+          tc_fence_after();
+        }
+        // ---- the rows' results: complete, or a part of an item that other blocks work on too ----
+        const int c0 = (int)(w.item0 / share), c1 = (int)((w.item0 + w.it.n - 1) / share);
+        const size_t part = (size_t)(2 * blockIdx.x + (w.item0 < u0 ? 0 : 1)) * 256;
+        const auto out_row = [&](int i, int hh) {
+          return a.o.data + w.b * a.o.seq + (long long)(w.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
+        };
+        if (active && *reinterpret_cast<volatile int*>(&sm.odd[w.count & 3])) {
+          // rare: what the operands could not hold, row by row; this warp's rows of the query tile are free as scratch
+          float* qs = reinterpret_cast<float*>(sm.q[slot] + (warp & 3) * 32 * 128);
+          for (int rr = 0; rr < 32; ++rr) {
+            const int ir = slot * kRows + (warp & 3) * 32 + rr;
+            if (ir >= w.it.rows) break;
+            const int gr = 256 * w.p + ir, i = gr / a.group, hh = w.h * a.group + gr - i * a.group;
+            const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(
+                a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row + (long long)hh * a.q.head);
+            for (int c = lane; c < D; c += 32) qs[c] = to_f32(q[c]);
+            __syncwarp();
+            int f0, l0;
+            visible(a, w.s.len, w.s.len - w.s.n + i, &f0, &l0);
+            float mr, lr, acc[D / 32];
+            row_attention<typename std::conditional<kF8, uint8_t, __nv_bfloat16>::type, D>(
+                a, w.b, w.h, qs, max(f0, w.t_begin * kKeys), min(l0, w.t_end * kKeys), &mr, &lr, acc);
+            __syncwarp();
+            const float inv = lr == 0.f ? 0.f : 1.f / lr;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              if (c0 == c1) reinterpret_cast<__nv_bfloat16*>(out_row(i, hh))[c * 32 + lane] = from_f32<__nv_bfloat16>(acc[c] * inv);
+              else p.part_o[(part + ir) * D + c * 32 + lane] = acc[c];
+            }
+            if (lane == 0) {
+              float* lse = lse_at(a, w.b, w.s, i, hh);
+              if (c0 != c1) p.part_ml[part + ir] = make_float2(mr, lr);
+              else if (lse) *lse = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
+            }
+          }
+        } else if (active) {
+          const float unit = kF8 ? pow2(sm.unit[w.count & 3][1]) : 1.f;      // O's
+          const float inv = (l == 0.f ? 0.f : 1.f / l) * unit;
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            float ov[32];
+            __syncwarp();
+            tmem_ld32(to + 32 * ch, ov);
+            tmem_ld_wait();
+            if (!valid) {
+            } else if (c0 == c1) {
+              uint4* dst = reinterpret_cast<uint4*>(out_row(tok, head) + 64 * ch);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                dst[x] = make_uint4(pack_bf16x2(ov[8 * x] * inv, ov[8 * x + 1] * inv), pack_bf16x2(ov[8 * x + 2] * inv, ov[8 * x + 3] * inv),
+                                    pack_bf16x2(ov[8 * x + 4] * inv, ov[8 * x + 5] * inv), pack_bf16x2(ov[8 * x + 6] * inv, ov[8 * x + 7] * inv));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + (part + row) * D + 32 * ch);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                dst[x] = make_float4(ov[4 * x] * unit, ov[4 * x + 1] * unit, ov[4 * x + 2] * unit, ov[4 * x + 3] * unit);
+            }
+          }
+          if (valid) {
+            if (c0 != c1) p.part_ml[part + row] = make_float2(m, l);
+            else if (float* lse = lse_at(a, w.b, w.s, tok, head)) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          }
+          tc_fence_before();             // O is read before the next item's first product overwrites it
+        }
+        if (c0 != c1) {
+          __threadfence();
+          softmax_sync();
+          if (threadIdx.x == 0) {
+            const bool done = atomicAdd(p.counters + c0, 1) == c1 - c0;
+            if (done) p.counters[c0] = 0;                       // as the next call finds it
+            sm.last = done;
+          }
+          softmax_sync();
+          if (sm.last) {
+            __threadfence();
+            constexpr int kLanes = D / 4;                       // threads a row, four columns each
+            for (int ir = threadIdx.x / kLanes; ir < w.it.rows; ir += kSoftmax / kLanes) {
+              const int col = (threadIdx.x % kLanes) * 4;
+              float mm = -INFINITY;
+              for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(&p.part_ml[(size_t)(2 * c + (c == c0)) * 256 + ir]).x);
+              const float base2 = mm == -INFINITY ? 0.f : mm;
+              float ll = 0.f;
+              float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+              for (int c = c0; c <= c1; ++c) {
+                const size_t at = (size_t)(2 * c + (c == c0)) * 256 + ir;
+                const float2 ml = __ldcg(&p.part_ml[at]);
+                const float4 po = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + col));
+                const float f = ex2(ml.x - base2);
+                ll = fmaf(ml.y, f, ll);
+                o.x = fmaf(po.x, f, o.x);
+                o.y = fmaf(po.y, f, o.y);
+                o.z = fmaf(po.z, f, o.z);
+                o.w = fmaf(po.w, f, o.w);
+              }
+              const int gr = 256 * w.p + ir, i = gr / a.group, hh = w.h * a.group + gr - i * a.group;
+              const float inv = ll == 0.f ? 0.f : 1.f / ll;
+              *reinterpret_cast<uint2*>(out_row(i, hh) + col * 2) =
+                  make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+              float* lse = lse_at(a, w.b, w.s, i, hh);
+              if (lse && col == 0) *lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+            }
+          }
+          softmax_sync();                // sm.last is read
+        }
+        ++w.count;
+      } while (next());
+    } else if (warp < 12) {
+      // =========================== values made ready ===========================
+      const int r = threadIdx.x & 127;   // my key of the tile
+      uint32_t n_tile = 0;
+      do {
+        if (w.t_begin >= w.t_end) continue;
+        const int it4 = w.count & 3;
+        if (r == 0) sm.odd[it4] = 0;
+        aux_sync();
+        // keys that all of the item's rows see: tiles inside need no care
+        int f0, l0, f1, l1;
+        visible(a, w.s.len, w.s.len - w.s.n + 256 * w.p / a.group, &f0, &l0);
+        visible(a, w.s.len, w.s.len - w.s.n + (256 * w.p + w.it.rows - 1) / a.group, &f1, &l1);
+        const int all_first = max(f0, f1), all_last = min(l0, l1);
+        int eu[2] = {0, 0};              // E of K and of V
+        for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
+          const int st = n_tile & 1;
+          const uint32_t ph = (n_tile >> 1) & 1;
+          if constexpr (!kF8) {
+            wait(sm, &sm.vfull[st], ph, p);
+            const uint32_t* bad = sm.bad[n_tile & 3];
+            if (t * kKeys < all_first || (t + 1) * kKeys > all_last || (bad[0] | bad[1] | bad[2] | bad[3])) {
+              const bool there = t * kKeys + r < w.s.len && !((bad[r >> 5] >> (r & 31)) & 1u);
+              bool odd = false;
+#pragma unroll 4
+              for (int c = 0; c < D / 8; ++c) {
+                uint4* x = reinterpret_cast<uint4*>(sm.v[st] + (c >> 3) * S::kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                uint4 u = there ? *x : make_uint4(0, 0, 0, 0);
+                uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((y[e] & 0x7f80u) == 0x7f80u) { odd = true; y[e] &= 0xffff0000u; }
+                  if ((y[e] & 0x7f800000u) == 0x7f800000u) { odd = true; y[e] &= 0x0000ffffu; }
+                }
+                *x = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+              if (odd) *reinterpret_cast<volatile int*>(&sm.odd[it4]) = 1;
+              fence_async_shared();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.vready[st]);
+          } else {
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side) {
+              wait(sm, &sm.rawfull[side], n_tile & 1, p);
+              const uint32_t* bad = sm.bad[n_tile & 3];
+              const bool there = t * kKeys + r < w.s.len && !((bad[r >> 5] >> (r & 31)) & 1u);
+              const int e = there ? (int)sm.raw_exp[side][r] - kExpBias : -kExpLimit;
+              if (t == w.t_begin) {      // the unit of the share: the first tile's largest exponent
+                const int mx = __reduce_max_sync(FULL, e);
+                if (lane == 0) sm.red[warp - 8] = mx;
+                aux_sync();
+                eu[side] = max(max(sm.red[0], sm.red[1]), max(sm.red[2], sm.red[3]));
+                if (r == 0) sm.unit[it4][side] = eu[side];
+                aux_sync();
+              }
+              const int de = e - eu[side];
+              const bool far = de > kAbove || de < -kBelow;
+              const __half f16 = __float2half_rn(there ? pow2(max(-24, min(kAbove, de))) : 0.f);
+              const __half2 f2 = __half2half2(f16);
+              // the converted stage is free
+              if (n_tile >= kStages) wait(sm, side ? &sm.vempty[st] : &sm.kempty[st], ph ^ 1u, p);
+              uint8_t* dst = side ? sm.v[st] : sm.k[st];
+              const bool edge = t * kKeys < all_first || (t + 1) * kKeys > all_last;
+              bool odd = false;
+#pragma unroll 2
+              for (int c = 0; c < D / 16; ++c) {
+                const int cs = D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+                const uint4 u = *reinterpret_cast<const uint4*>(sm.raw[side] + r * D + cs * 16);
+                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t h = e4m3x2_to_f16x2((uint16_t)(x[i >> 1] >> (16 * (i & 1))));
+                  const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&h), f2);
+                  y[i] = *reinterpret_cast<const uint32_t*>(&z);
+                }
+                if (there && far && (x[0] | x[1] | x[2] | x[3])) odd = true;
+                if (!there) {            // a stale NaN times zero
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) y[i] = 0u;
+                } else if (edge && side) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if ((y[i] & 0x7c00u) == 0x7c00u || (y[i] & 0x7c000000u) == 0x7c000000u) { odd = true; y[i] = 0u; }
+                }
+                uint8_t* row = dst + (c >> 2) * S::kHalf + r * 128;
+                const int ch = (2 * c) & 7;
+                *reinterpret_cast<uint4*>(row + ((ch ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+              }
+              if (odd) *reinterpret_cast<volatile int*>(&sm.odd[it4]) = 1;
+              fence_async_shared();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&sm.rawempty[side]);
+                mbar_arrive(side ? &sm.vready[st] : &sm.kfull[st]);
+              }
+            }
+          }
+        }
+        ++w.count;
+      } while (next());
+    } else if (warp == 12) {
+      // =============================== producer ===============================
+      if (lane == 0) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+      }
+      const int box = a.pool.page, boxes = kKeys / box;
+      constexpr int kHalves = kF8 ? 1 : D / 64;
+      const uint32_t box_bytes = (uint32_t)box * D * (kF8 ? 1 : 2) + (kF8 ? (uint32_t)box : 0u);
+      uint32_t n_tile = 0;
+      do {
+        for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
+          const int st = n_tile & 1;
+          const uint32_t ph = (n_tile >> 1) & 1;
+          int row = -1;                  // lane i < boxes: the box's first row of the pool
+          const int pos = t * kKeys + lane * box;
+          if (lane < boxes && pos < w.s.len && pos + box > w.it.first) {
+            const int pg = load_page(a.seqs, a.pool, w.b, pos);
+            if (pg >= 0) row = (pg * a.pool.kv_heads + w.h) * box;
+          }
+          const unsigned have = __ballot_sync(FULL, row >= 0);
+#pragma unroll 1
+          for (int side = 0; side < 2; ++side) {
+            uint64_t* full = kF8 ? &sm.rawfull[side] : side ? &sm.vfull[st] : &sm.kfull[st];
+            if (kF8) {
+              if (n_tile >= 1) wait(sm, &sm.rawempty[side], (n_tile - 1) & 1, p);
+            } else if (n_tile >= kStages) {
+              wait(sm, side ? &sm.vempty[st] : &sm.kempty[st], ph ^ 1u, p);
+            }
+            if (side == 0 && lane < 4) { // the tile's missing keys, before anything of it is released
+              uint32_t bits = 0;
+              for (int i = 0; i < 32; i += 16) {
+                const int at = (lane * 32 + i) / box;
+                if (!((have >> at) & 1u)) bits |= 0xffffu << i;
+              }
+              sm.bad[n_tile & 3][lane] = bits;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(full, __popc(have) * box_bytes);
+            __syncwarp();
+            const int i = lane / kHalves, half = lane % kHalves;        // boxes * halves <= 16
+            const int rr = __shfl_sync(FULL, row, i);
+            if (i < boxes && rr >= 0) {
+              uint8_t* dst = kF8 ? sm.raw[side] + i * box * D
+                                 : (side ? sm.v[st] : sm.k[st]) + half * S::kHalf + i * box * 128;
+              tma_load_3d(dst, side ? &vmap : &kmap, full, half * 64, rr, 0);
+              if (kF8) bulk_load(sm.raw_exp[side] + i * box, (side ? a.pool.v_exp : a.pool.k_exp) + rr, box, full);
+            }
+          }
+        }
+      } while (next());
+      // every copy lands before this block's shared memory is released
+      if (lane == 0)
+        for (uint32_t i = n_tile > kStages ? n_tile - kStages : 0; i < n_tile; ++i) {
+          if (kF8) {
+            if (i + 1 == n_tile)
+              for (int side = 0; side < 2; ++side) mbar_drain(&sm.rawfull[side], i & 1, p.wait_ns);
+          } else {
+            mbar_drain(&sm.kfull[i & 1], (i >> 1) & 1, p.wait_ns);
+            mbar_drain(&sm.vfull[i & 1], (i >> 1) & 1, p.wait_ns);
+          }
+        }
+    } else if (warp == 13 && lane == 0) {
+      // =============================== MMA issuer ===============================
+      constexpr uint32_t idesc_s = kF8 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_pv = kF8 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
+      uint32_t n_tile = 0, n_slot[2] = {0, 0}, n_item[2] = {0, 0};
+      const auto scores = [&](int slot, int st) {
+        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[slot]), 16, 1024), kd = smem_desc_sw128(smem_u32(sm.k[st]), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + 128 * slot, qd + off, kd + off, idesc_s, kk > 0);
+        }
+        mma_commit(&sm.sfull[slot]);
+      };
+      const auto values = [&](int slot, int st, bool fresh) {
+        const uint32_t par = n_slot[slot] & 1;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          wait(sm, &sm.pfull[slot][hh], par, p);
+          tc_fence_after();
+          const uint64_t vd = smem_desc_sw128(smem_u32(sm.v[st]) + 8192 * hh, S::kHalf, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tmem + kColO + 128 * slot, tmem + 128 * slot + 64 * hh + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), idesc_pv,
+                   (!fresh || hh > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&sm.odone[slot][hh]);
+        }
+        ++n_slot[slot];
+      };
+      do {
+        if (w.t_begin >= w.t_end) continue;
+        const int slots = w.it.rows > kRows ? 2 : 1;
+        for (int s = 0; s < slots; ++s) wait(sm, &sm.qfull[s], n_item[s]++ & 1, p);
+        wait(sm, &sm.kfull[n_tile & 1], (n_tile >> 1) & 1, p);
+        tc_fence_after();
+        for (int s = 0; s < slots; ++s) scores(s, n_tile & 1);
+        mma_commit(&sm.kempty[n_tile & 1]);
+        for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
+          const int st = n_tile & 1, nst = st ^ 1;
+          const bool more = t + 1 < w.t_end;
+          wait(sm, &sm.vready[st], (n_tile >> 1) & 1, p);
+          tc_fence_after();
+          for (int s = 0; s < slots; ++s) {
+            values(s, st, t == w.t_begin);
+            if (s + 1 == slots) mma_commit(&sm.vempty[st]);
+            if (more) {
+              if (s == 0) {
+                wait(sm, &sm.kfull[nst], ((n_tile + 1) >> 1) & 1, p);
+                tc_fence_after();
+              }
+              scores(s, nst);
+              if (s + 1 == slots) mma_commit(&sm.kempty[nst]);
+            }
+          }
+        }
+      } while (next());
+      mma_commit(&sm.drain);
+      mbar_drain(&sm.drain, 0, p.wait_ns);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  __syncwarp();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool kF8>
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const size_t smem = sizeof(Smem<D, kF8>) + 1024;
+  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk<D, kF8>), smem))) return e;
+  attn_chunk<D, kF8><<<min(sms, kMaxChunkBlocks), kThreads, smem, st>>>(km, vm, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned long long wait_ns, cudaStream_t st) {
+  CUtensorMap km, vm;
+  const uint64_t rows = (uint64_t)a.pool.num_pages * a.pool.kv_heads * a.pool.page;
+  const int esz = a.pool.dtype == PISA_CACHE_E4M3 ? 1 : 2;
+  if (!encode_rows(&km, a.pool.k, esz, d, rows, a.pool.page) || !encode_rows(&vm, a.pool.v, esz, d, rows, a.pool.page))
+    return cudaErrorInvalidValue;
+  Params p;
+  p.a = a;
+  char* w = static_cast<char*>(ws);
+  p.counters = reinterpret_cast<int*>(w + kCountersAt);
+  p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
+  p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxChunkBlocks * kMaxChunkRows);
+  p.item_cost = 2;
+  p.wait_ns = wait_ns;
+  if (esz == 1) return d == 64 ? launch<64, true>(km, vm, p, st) : launch<128, true>(km, vm, p, st);
+  return d == 64 ? launch<64, false>(km, vm, p, st) : launch<128, false>(km, vm, p, st);
+}
+
+}  // namespace cache
+}  // namespace pisa

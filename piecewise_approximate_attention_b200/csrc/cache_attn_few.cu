@@ -104,15 +104,16 @@ struct Params {
 // takes n places for its tiles and then p.item_cost for what it costs besides them; cost = 0 if n = 0.
 struct Item {
   Seq s;
-  int t0, n;
+  int t0, n, first;             // first: the first key that any row sees
   long long cost;
 };
 __device__ __forceinline__ Item load_item(const AttnArgs& a, int b, int item_cost) {
   Item it;
-  it.t0 = it.n = 0;
+  it.t0 = it.n = it.first = 0;
   it.cost = 0;
   if (!load_seq(a.seqs, b, a.q.rows, &it.s) || it.s.n == 0) return it;
   const int first = a.window > 0 ? max(0, min(it.s.len, it.s.len - it.s.n - a.window + 1)) : 0;
+  it.first = first;
   it.t0 = first / kTile;
   it.n = max(1, (it.s.len + kTile - 1) / kTile - it.t0);      // an empty sequence's rows are written too
   it.cost = it.n + item_cost;
@@ -240,7 +241,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
         // lane i < pages looks box i's page up
         int row = -1;
         const int pos = t * kTile + lane * box;
-        if (lane < pages && pos < it.s.len) {
+        if (lane < pages && pos < it.s.len && pos + box > it.first) {
           const int pg = load_page(a.seqs, a.pool, b, pos);
           if (pg >= 0) row = (pg * a.pool.kv_heads + h) * a.pool.page + (pos & (a.pool.page - 1));
         }

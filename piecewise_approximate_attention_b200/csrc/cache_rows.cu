@@ -42,7 +42,7 @@ __device__ __forceinline__ uint2 quantise(uint4 u, uint8_t* exp_byte) {
   for (int d = D / 16; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   // m = f * 2^E, 448 = 1.75 * 2^8: the smallest e with m <= 448 * 2^e is E - 8 if f <= 1.75, else E - 7
   int e = (int)((m + 0x1fffffu) >> 23) - 8 - kExpBias;
-  e = m == 0u ? 0 : max(-kExpLimit, min(kExpLimit, e));
+  e = max(-kExpLimit, min(kExpLimit, e));
   const float inv = pow2(-e);
   uint32_t c[4];
 #pragma unroll

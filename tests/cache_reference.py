@@ -1,8 +1,7 @@
 """The paged cache's operators from their definition, in float64 on the CPU, and how far the kernels
 may be from it.
 
-Stored e4m3 rows: value = code * 2^e with the smallest e for which max|x| <= 448 * 2^e, |e| <= 50 (0 for a
-row of zeros), code = x * 2^-e rounded to nearest even to three fraction bits (steps of 2^-9 below 2^-6).
+Stored e4m3 rows: value = code * 2^e with the smallest e for which max|x| <= 448 * 2^e, |e| <= 50, code = x * 2^-e rounded to nearest even to three fraction bits (steps of 2^-9 below 2^-6).
 """
 import math
 
@@ -19,7 +18,6 @@ def quantise(x):
     e = torch.full_like(top, -50.0)
     while bool((more := (top > 448.0 * torch.exp2(e)) & (e < 50)).any()):
         e = torch.where(more, e + 1, e)
-    e = torch.where(top == 0, torch.zeros_like(e), e)
     y = (x / torch.exp2(e)).clamp(-448.0, 448.0)
     step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
     return torch.round(y / step) * step * torch.exp2(e), e[..., 0]
