@@ -9,8 +9,8 @@
 //
 // Block (one an SM, 16 warps):
 //   warps 0-3, 4-7   softmax and output of slot 0 and 1: thread r owns row r (TMEM lane r).  Per tile
-//                    and half of 64 keys: scores from TMEM, running maximum (moved only when a row
-//                    outgrows it by 2^8), P back over the scores' columns, release to the MMA warp
+//                    and half of 64 keys: scores from TMEM, weights against a maximum that is moved only
+//                    when a row outgrows it by 2^15, P back over the scores' columns, release to warp 13
 //   warps 8-11       values made ready: see below; thread r owns key r of the tile
 //   warp 12          follows the page table, TMA loads into two K and two V stages
 //   warp 13          issues the MMAs: S = Q K^T (M 128, N 128), O += P V per half (P from TMEM), the slots in
@@ -41,7 +41,7 @@ constexpr int kKeys = 128;                   // keys of a tile
 constexpr int kRows = 128;                   // rows of a slot
 constexpr int kThreads = 512;
 constexpr int kSoftmax = 256;
-constexpr float kLazyLog2 = 8.f;
+constexpr float kRoom = 32768.f;              // weights of a half that P (fp16 at least) takes as they are
 constexpr unsigned FULL = 0xffffffffu;
 constexpr uint32_t kColO = 256;
 constexpr int kStages = 2;
@@ -380,56 +380,65 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
 #pragma unroll
                 for (int x = 0; x < 32; ++x) s[32 + x] = ((vm1 >> x) & 1u) ? s[32 + x] : -INFINITY;
               }
-              float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]), t2 = fmaxf(s[4], s[5]), t3 = fmaxf(s[6], s[7]);
+              // Weights against the maximum so far, without looking for the half's own first: their sum says
+              // whether a row outgrew it (each weight is at most the sum, so below kRoom P holds them all).
+              float ls = 0.f;
+              const auto weights = [&]() {
+                const float mb = m == -INFINITY ? 0.f : m;
+                const uint64_t sc2 = f2_pack(sl, sl), nmb2 = f2_pack(-mb, -mb);
+                uint64_t acc2 = f2_pack(0.f, 0.f);
 #pragma unroll
-              for (int c = 8; c < 64; c += 8) {
-                t0 = fmax3(t0, s[c], s[c + 1]);
-                t1 = fmax3(t1, s[c + 2], s[c + 3]);
-                t2 = fmax3(t2, s[c + 4], s[c + 5]);
-                t3 = fmax3(t3, s[c + 6], s[c + 7]);
-              }
-              const float m_new = fmaxf(m, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sl);      // base-2 units
-              const bool grow = m_new > m + kLazyLog2;
-              const float f = grow ? ex2(m - m_new) : 1.f;     // 0 when m = -inf
-              if (grow) {
+                for (int ch = 0; ch < 2; ++ch) {
+                  uint32_t pk[16];
+#pragma unroll
+                  for (int x = 0; x < 32; x += 2) {
+                    const int c = 32 * ch + x;
+                    float x0, x1;
+                    f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nmb2), x0, x1);
+                    const float p0 = ex2(x0), p1 = ex2(x1);
+                    acc2 = f2_add(acc2, f2_pack(p0, p1));
+                    pk[x >> 1] = kF8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                  }
+                  tmem_st16(ts + 64 * hh + 16 * ch, pk);
+                }
+                float ls0, ls1;
+                f2_unpack(acc2, ls0, ls1);
+                ls = ls0 + ls1;
+              };
+              const bool first_half = t == w.t_begin && hh == 0;
+              if (!first_half) weights();
+              if (__any_sync(FULL, first_half || ls > kRoom || m == -INFINITY)) {
+                // rare but for the first half: move the maximum, and with it l and O
+                float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]), t2 = fmaxf(s[4], s[5]), t3 = fmaxf(s[6], s[7]);
+#pragma unroll
+                for (int c = 8; c < 64; c += 8) {
+                  t0 = fmax3(t0, s[c], s[c + 1]);
+                  t1 = fmax3(t1, s[c + 2], s[c + 3]);
+                  t2 = fmax3(t2, s[c + 4], s[c + 5]);
+                  t3 = fmax3(t3, s[c + 6], s[c + 7]);
+                }
+                const float m_new = fmaxf(m, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sl);      // base-2 units
+                const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);         // 0 when m = -inf
                 l *= f;
                 m = m_new;
-              }
-              const float mb = m == -INFINITY ? 0.f : m;
-              const uint64_t sc2 = f2_pack(sl, sl), nmb2 = f2_pack(-mb, -mb);
-              uint64_t acc2 = f2_pack(0.f, 0.f);
+                if (!first_half) {
+                  // O holds the products of the halves before this one
+                  wait(sm, &sm.odone[slot][hh ^ 1], hh ? par : par ^ 1u, p);
+                  __syncwarp();
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int ch = 0; ch < D / 16; ++ch) {
+                    float ov[16];
+                    tmem_ld16(to + 16 * ch, ov);
+                    tmem_ld_wait();
 #pragma unroll
-              for (int ch = 0; ch < 2; ++ch) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                  const int c = 32 * ch + x;
-                  float x0, x1;
-                  f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nmb2), x0, x1);
-                  const float p0 = ex2(x0), p1 = ex2(x1);
-                  acc2 = f2_add(acc2, f2_pack(p0, p1));
-                  pk[x >> 1] = kF8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                    for (int x = 0; x < 16; ++x) ov[x] *= f;
+                    tmem_st16(to + 16 * ch, reinterpret_cast<const uint32_t*>(ov));
+                  }
                 }
-                tmem_st16(ts + 64 * hh + 16 * ch, pk);
+                weights();
               }
-              float ls0, ls1;
-              f2_unpack(acc2, ls0, ls1);
-              l += ls0 + ls1;
-              // O holds the products of the halves before this one: it is scaled before this half's P is released
-              if (__any_sync(FULL, grow) && (t > w.t_begin || hh > 0)) {
-                wait(sm, &sm.odone[slot][hh ^ 1], hh ? par : par ^ 1u, p);
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll
-                for (int ch = 0; ch < D / 32; ++ch) {
-                  float ov[32];
-                  tmem_ld32(to + 32 * ch, ov);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int x = 0; x < 32; ++x) ov[x] *= f;
-                  tmem_st32(to + 32 * ch, ov);
-                }
-              }
+              l += ls;
               tmem_st_wait();
               tc_fence_before();
               mbar_arrive(&sm.pfull[slot][hh]);
