@@ -121,12 +121,13 @@ __device__ __forceinline__ float* lse_at(const AttnArgs& a, int b, const Seq& s,
                        : a.lse + ((size_t)b * a.heads + h) * a.q.rows + i;
 }
 
-// Workspace: status word, counters of the blocks (zero between calls), partial results of items that
-// several blocks share: per block two of them (the end of one item, the beginning of another).
+// Workspace: status word, counters of the few-row kernel's blocks (zero between calls), words for the
+// chunk kernel's joining, partial results of items that several blocks share: per block two of them (the end of one item, the beginning of another).
 constexpr int kMaxFewBlocks = 296, kMaxFewRows = 64;       // few-row attention: two blocks on each of 148 SMs
 constexpr size_t kCountersAt = kStatusBytes;
-constexpr size_t kPartialsAt = kCountersAt + (kMaxFewBlocks * sizeof(int) + 255) / 256 * 256;
+constexpr size_t kSplitAt = kCountersAt + (kMaxFewBlocks * sizeof(int) + 255) / 256 * 256;
 constexpr int kMaxChunkBlocks = 148, kMaxChunkRows = 256;  // chunk attention: one block an SM
+constexpr size_t kPartialsAt = kSplitAt + (kMaxChunkBlocks * sizeof(int4) + 255) / 256 * 256;
 inline size_t partials_bytes(int d) {
   const size_t few = (size_t)kMaxFewBlocks * kMaxFewRows, chunk = (size_t)kMaxChunkBlocks * kMaxChunkRows;
   return 2 * (few > chunk ? few : chunk) * (d + 2) * sizeof(float);

@@ -5,7 +5,7 @@
 // of 128 that walk the same tiles of 128 keys together, so a key tile is read from L2 once for 256
 // rows, and one slot's softmax runs while the tensor core works on the other's products.  As in the
 // few-row kernel all items' key tiles form one line that is cut into equal shares, one a block, and
-// items that several blocks share are joined through the workspace by the block that ends last.
+// items that several blocks share leave partial results (O, maximum, sum) that a second small kernel joins.
 //
 // Block (one an SM, 16 warps):
 //   warps 0-3, 4-7   softmax and output of slot 0 and 1: thread r owns row r (TMEM lane r).  Per tile
@@ -40,14 +40,12 @@ using namespace sm100;
 constexpr int kKeys = 128;                   // keys of a tile
 constexpr int kRows = 128;                   // rows of a slot
 constexpr int kThreads = 512;
-constexpr int kSoftmax = 256;
 constexpr float kRoom = 32768.f;              // weights of a half that P (fp16 at least) takes as they are
 constexpr unsigned FULL = 0xffffffffu;
 constexpr uint32_t kColO = 256;
 constexpr int kStages = 2;
 constexpr int kBelow = 15, kAbove = 7;       // exponents that fp16 holds exactly around E
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -72,14 +70,14 @@ struct alignas(1024) Smem {
   int red[4];
   long long scan[kThreads / 32], before;
   uint32_t tmem;
-  int abort, last, start_b, start_h, start_p;
+  int abort, start_b, start_h, start_p;
 };
 
 struct Params {
   AttnArgs a;
-  int* counters;             // one a block, zero between calls
+  int4* split;               // one a block: the item that begins in it and is shared (sequence, head, pair, parts), parts = 0 for none
   float2* part_ml;           // [2 * blocks][256]
-  float* part_o;             // [2 * blocks][256][D]
+  float* part_o;             // [2 * blocks][D / 4][256][4]: a warp's rows next to one another
   int item_cost;
   unsigned long long wait_ns;
 };
@@ -152,10 +150,10 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       mbar_init(&sm.vready[i], 4);
       mbar_init(&sm.rawfull[i], 1);
       mbar_init(&sm.rawempty[i], 4);
-      mbar_init(&sm.qfull[i], kRows);
+      mbar_init(&sm.qfull[i], 4);
       mbar_init(&sm.sfull[i], 1);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(&sm.pfull[i][h], kRows);
+        mbar_init(&sm.pfull[i][h], 4);
         mbar_init(&sm.odone[i][h], 1);
       }
     }
@@ -184,6 +182,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) total += sm.scan[w];
@@ -331,8 +330,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             *reinterpret_cast<uint4*>(sm.q[slot] + (c >> 3) * S::kHalf + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = u;
           }
           fence_async_shared();
-          mbar_arrive(&sm.qfull[slot]);
           __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.qfull[slot]);
           // keys that all of the warp's rows see
           int all_first = first, all_last = last;
 #pragma unroll
@@ -364,7 +363,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
                   tmem_st16(ts + 64 * hh + 16, zero);
                   tmem_st_wait();
                   tc_fence_before();
-                  mbar_arrive(&sm.pfull[slot][hh]);
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&sm.pfull[slot][hh]);
                   continue;
                 }
               }
@@ -441,7 +441,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               l += ls;
               tmem_st_wait();
               tc_fence_before();
-              mbar_arrive(&sm.pfull[slot][hh]);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.pfull[slot][hh]);
             }
           }
           wait(sm, &sm.odone[slot][1], (n_tile - 1) & 1, p);
@@ -475,7 +476,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               if (c0 == c1) reinterpret_cast<__nv_bfloat16*>(out_row(i, hh))[c * 32 + lane] = from_f32<__nv_bfloat16>(acc[c] * inv);
-              else p.part_o[(part + ir) * D + c * 32 + lane] = acc[c];
+              else p.part_o[part * D + ((c * 32 + lane) / 4 * kMaxChunkRows + ir) * 4 + lane % 4] = acc[c];
             }
             if (lane == 0) {
               float* lse = lse_at(a, w.b, w.s, i, hh);
@@ -500,10 +501,10 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
                 dst[x] = make_uint4(pack_bf16x2(ov[8 * x] * inv, ov[8 * x + 1] * inv), pack_bf16x2(ov[8 * x + 2] * inv, ov[8 * x + 3] * inv),
                                     pack_bf16x2(ov[8 * x + 4] * inv, ov[8 * x + 5] * inv), pack_bf16x2(ov[8 * x + 6] * inv, ov[8 * x + 7] * inv));
             } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + (part + row) * D + 32 * ch);
+              float4* dst = reinterpret_cast<float4*>(p.part_o + part * D) + 8 * ch * kMaxChunkRows + row;
 #pragma unroll
               for (int x = 0; x < 8; ++x)
-                dst[x] = make_float4(ov[4 * x] * unit, ov[4 * x + 1] * unit, ov[4 * x + 2] * unit, ov[4 * x + 3] * unit);
+                dst[x * kMaxChunkRows] = make_float4(ov[4 * x] * unit, ov[4 * x + 1] * unit, ov[4 * x + 2] * unit, ov[4 * x + 3] * unit);
             }
           }
           if (valid) {
@@ -512,68 +513,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           }
           tc_fence_before();             // O is read before the next item's first product overwrites it
         }
-        if (c0 != c1) {
-          __threadfence();
-          softmax_sync();
-          if (threadIdx.x == 0) {
-            const bool done = atomicAdd(p.counters + c0, 1) == c1 - c0;
-            if (done) p.counters[c0] = 0;                       // as the next call finds it
-            sm.last = done;
-          }
-          softmax_sync();
-          if (sm.last) {
-            __threadfence();
-            // thread i: row i's maximum and sum over the parts; then eight rows at a time, a warp a row
-            const int parts = c1 - c0 + 1;
-            const auto slot_of = [&](int x) { return (size_t)(2 * (c0 + x) + (x == 0)) * 256; };
-            const int ir = threadIdx.x;
-            float mm = -INFINITY, ll = 0.f;
-            for (int x = 0; x < parts; ++x) mm = fmaxf(mm, __ldcg(&p.part_ml[slot_of(x) + ir]).x);
-            const float base2 = mm == -INFINITY ? 0.f : mm;
-            for (int x = 0; x < parts; ++x) {
-              const float2 ml = __ldcg(&p.part_ml[slot_of(x) + ir]);
-              ll = fmaf(ml.y, ex2(ml.x - base2), ll);
-            }
-            float2* join = reinterpret_cast<float2*>(sm.q[0]);     // the queries are done with
-            join[ir] = make_float2(base2, ll == 0.f ? 0.f : 1.f / ll);
-            if (ir < w.it.rows && a.lse) {
-              const int gr = 256 * w.p + ir, i = gr / a.group;
-              *lse_at(a, w.b, w.s, i, w.h * a.group + gr - i * a.group) =
-                  ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
-            }
-            softmax_sync();
-            constexpr int kLanes = D / 4, kStep = kSoftmax / kLanes, kBatch = 8;   // threads a row, four columns each
-            const int col = (threadIdx.x % kLanes) * 4;
-            for (int r0 = threadIdx.x / kLanes; r0 < w.it.rows; r0 += kBatch * kStep) {
-              float4 o[kBatch];
-#pragma unroll
-              for (int y = 0; y < kBatch; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-              for (int x = 0; x < parts; ++x) {
-#pragma unroll
-                for (int y = 0; y < kBatch; ++y) {
-                  const int rr = r0 + y * kStep;
-                  if (rr >= w.it.rows) break;
-                  const float f = ex2(__ldcg(&p.part_ml[slot_of(x) + rr]).x - join[rr].x);
-                  const float4 po = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot_of(x) + rr) * D + col));
-                  o[y].x = fmaf(po.x, f, o[y].x);
-                  o[y].y = fmaf(po.y, f, o[y].y);
-                  o[y].z = fmaf(po.z, f, o[y].z);
-                  o[y].w = fmaf(po.w, f, o[y].w);
-                }
-              }
-#pragma unroll
-              for (int y = 0; y < kBatch; ++y) {
-                const int rr = r0 + y * kStep;
-                if (rr >= w.it.rows) break;
-                const int gr = 256 * w.p + rr, i = gr / a.group, hh = w.h * a.group + gr - i * a.group;
-                const float inv = join[rr].y;
-                *reinterpret_cast<uint2*>(out_row(i, hh) + col * 2) =
-                    make_uint2(pack_bf16x2(o[y].x * inv, o[y].y * inv), pack_bf16x2(o[y].z * inv, o[y].w * inv));
-              }
-            }
-          }
-          softmax_sync();                // sm.last is read
-        }
+        // the block that begins an item which others go on with leaves word of it for the joining kernel
+        if (threadIdx.x == 0 && c0 != c1 && w.item0 >= u0) p.split[blockIdx.x] = make_int4(w.b, w.h, w.p, c1 - c0 + 1);
         ++w.count;
       } while (next());
     } else if (warp < 12) {
@@ -806,6 +747,53 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
   tc_fence_after();
   __syncwarp();
   if (warp == 13) tmem_dealloc(tmem, 512);
+  griddep_launch_dependents();
+}
+
+// Joins the parts of the items that several blocks worked on.  Block (i, y): the item that begins in
+// block i of the attention kernel, its rows [64 y, 64 y + 64), a warp 8 of them, a lane four columns of
+// one row at a time.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join(const Params p) {
+  griddep_wait();
+  const AttnArgs& a = p.a;
+  const int4 item = p.split[blockIdx.x];
+  if (item.w == 0) return;
+  const int b = item.x, h = item.y, parts = item.w, lane = threadIdx.x & 31;
+  Seq s;
+  if (!load_seq(a.seqs, b, a.q.rows, &s)) return;
+  const int r = blockIdx.y * 64 + (threadIdx.x >> 5) * 8 + (lane & 7);
+  if (256 * item.z + r >= s.n * a.group) return;
+  const auto slot_of = [&](int x) { return (size_t)(2 * (blockIdx.x + x) + (x == 0)) * kMaxChunkRows; };
+  float m = -INFINITY, l = 0.f;
+  for (int x = 0; x < parts; ++x) m = fmaxf(m, p.part_ml[slot_of(x) + r].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  float4 o[D / 16];
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int x = 0; x < parts; ++x) {
+    const float2 ml = p.part_ml[slot_of(x) + r];
+    const float f = ex2(ml.x - base);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + slot_of(x) * D) + (lane >> 3) * kMaxChunkRows + r;
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const float4 v = src[4 * c * kMaxChunkRows];
+      o[c].x = fmaf(v.x, f, o[c].x);
+      o[c].y = fmaf(v.y, f, o[c].y);
+      o[c].z = fmaf(v.z, f, o[c].z);
+      o[c].w = fmaf(v.w, f, o[c].w);
+    }
+  }
+  const int gr = 256 * item.z + r, i = gr / a.group, hh = h * a.group + gr - i * a.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2* dst = reinterpret_cast<uint2*>(a.o.data + b * a.o.seq + (long long)(s.row0 + i) * a.o.row + (long long)hh * a.o.head);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c)
+    dst[4 * c + (lane >> 3)] = make_uint2(pack_bf16x2(o[c].x * inv, o[c].y * inv), pack_bf16x2(o[c].z * inv, o[c].w * inv));
+  float* lse = lse_at(a, b, s, i, hh);
+  if (lse && lane < 8) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int D, bool kF8>
@@ -815,8 +803,20 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
   if (e != cudaSuccess) return e;
   const size_t smem = sizeof(Smem<D, kF8>) + 1024;
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk<D, kF8>), smem))) return e;
-  attn_chunk<D, kF8><<<min(sms, kMaxChunkBlocks), kThreads, smem, st>>>(km, vm, p);
-  return cudaGetLastError();
+  const int blocks = min(sms, kMaxChunkBlocks);
+  attn_chunk<D, kF8><<<blocks, kThreads, smem, st>>>(km, vm, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // scheduled early, it waits for the attention kernel (griddepcontrol.wait)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, kMaxChunkRows / 64);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join<D>, p);
 }
 
 }  // namespace
@@ -830,7 +830,7 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned 
   Params p;
   p.a = a;
   char* w = static_cast<char*>(ws);
-  p.counters = reinterpret_cast<int*>(w + kCountersAt);
+  p.split = reinterpret_cast<int4*>(w + kSplitAt);
   p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxChunkBlocks * kMaxChunkRows);
   p.item_cost = 2;
