@@ -136,7 +136,8 @@ inline size_t partials_bytes(int d) {
 // ---- launchers ----
 cudaError_t launch_append(const Pool& pool, int head_dim, const Seqs& seqs, const Rows& k, const Rows& v, cudaStream_t st);
 cudaError_t launch_read(const Pool& pool, int head_dim, const Seqs& seqs, const Rows& k, const Rows& v, cudaStream_t st);
-cudaError_t launch_attention_simt(const AttnArgs& a, int head_dim, cudaStream_t st);
+// fp32 pools.
+cudaError_t launch_attention_fp32(const AttnArgs& a, int head_dim, void* ws, cudaStream_t st);
 // bf16 and e4m3 pools, at most kMaxFewRows rows (new tokens times query heads of a key/value head).
 cudaError_t launch_attention_few(const AttnArgs& a, int head_dim, void* ws, unsigned long long wait_ns, cudaStream_t st);
 // bf16 and e4m3 pools, any number of rows.

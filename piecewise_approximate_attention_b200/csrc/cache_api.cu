@@ -97,7 +97,7 @@ extern "C" {
 
 size_t pisa_cache_workspace_bytes(const pisa_cache* c) {
   if (check_sizes(c) != PISA_OK) return 0;
-  return c->dtype == PISA_CACHE_FP32 ? kPartialsAt : kPartialsAt + partials_bytes(c->head_dim);
+  return kPartialsAt + partials_bytes(c->head_dim);
 }
 
 namespace {
@@ -154,7 +154,7 @@ pisa_status pisa_cache_attention(const pisa_cache* cache, const pisa_sequences* 
   a.window = window;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (cache->dtype == PISA_CACHE_FP32) return cuda_status(launch_attention_simt(a, cache->head_dim, st));
+  if (cache->dtype == PISA_CACHE_FP32) return cuda_status(launch_attention_fp32(a, cache->head_dim, ws, st));
   if ((long long)seqs->max_new * a.group <= kMaxFewRows)
     return cuda_status(launch_attention_few(a, cache->head_dim, ws, kWaitLimitNs, st));
   return cuda_status(launch_attention_chunk(a, cache->head_dim, ws, kWaitLimitNs, st));

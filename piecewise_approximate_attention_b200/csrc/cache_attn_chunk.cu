@@ -30,6 +30,7 @@
 // that do not), is flagged and its rows are computed by the plain routine of cache_row.cuh.  V rows of
 // stale slots and of missing pages are zeroed.
 #include "cache_row.cuh"
+#include "cache_walk.cuh"
 #include "sm100.cuh"
 
 namespace pisa {
@@ -68,9 +69,9 @@ struct alignas(1024) Smem {
   uint32_t bad[4][4];                                    // tile of the block & 3: keys whose page is missing
   int unit[4][2], odd[4];                                // item & 3: E of K and V; to be computed again
   int red[4];
-  long long scan[kThreads / 32], before;
+  WalkScratch<kThreads / 32> walk;
   uint32_t tmem;
-  int abort, start_b, start_h, start_p;
+  int abort;
 };
 
 struct Params {
@@ -81,28 +82,6 @@ struct Params {
   int item_cost;
   unsigned long long wait_ns;
 };
-
-// Rows [256 p, 256 p + rows) of a sequence and key/value head; their keys are tiles [t0, t0 + n).
-struct Item {
-  int t0, n, rows, first;             // first: the first key that any row sees
-  long long cost;
-};
-__device__ __forceinline__ int pairs_of(const AttnArgs& a, const Seq& s) { return (s.n * a.group + 255) / 256; }
-__device__ __forceinline__ Item item_of(const AttnArgs& a, const Seq& s, int p, int item_cost) {
-  Item it;
-  it.rows = min(256, s.n * a.group - 256 * p);
-  int f0, l0, f1, l1;
-  const int pos = s.len - s.n;
-  visible(a, s.len, pos + 256 * p / a.group, &f0, &l0);
-  visible(a, s.len, pos + (256 * p + it.rows - 1) / a.group, &f1, &l1);
-  // rows that see nothing (before the cache's first position) leave the range to the others
-  const int first = l0 > f0 ? f0 : 0, last = max(l0, l1);
-  it.first = first;
-  it.t0 = first / kKeys;
-  it.n = max(1, (last + kKeys - 1) / kKeys - it.t0);
-  it.cost = it.n + item_cost;
-  return it;
-}
 
 // After a timeout every wait returns at once and the block runs to its end on whatever its memory
 // holds (the status word says so), so that no warp is left at a barrier.
@@ -121,15 +100,6 @@ __device__ __forceinline__ uint32_t range_bits(int j0, int first, int last) {
   if (lo > 0) m &= lo >= 32 ? 0u : ~((1u << lo) - 1u);
   return m;
 }
-
-// Where a block is in the line of tiles; every role walks its own copy.
-struct Walk {
-  int b, h, p, pairs, count;          // count: items so far
-  Seq s;
-  Item it;
-  long long item0;
-  int t_begin, t_end;                 // this block's tiles of the item
-};
 
 template <int D, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -165,111 +135,13 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
-  // cost of a sequence and head: a warp a sequence, lanes over its row pairs
-  const auto seq_cost = [&](int b) -> long long {
-    Seq s;
-    long long c = 0;
-    if (b < a.seqs.batch && load_seq(a.seqs, b, a.q.rows, &s))
-      for (int i = lane; i < pairs_of(a, s); i += 32) c += item_of(a, s, i, p.item_cost).cost;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(FULL, c, d);
-    return c;
-  };
-  long long mine = 0;
-  for (int b = warp; b < a.seqs.batch; b += kThreads / 32) mine += seq_cost(b);
-  if (lane == 0) sm.scan[warp] = mine;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) total += sm.scan[w];
-  total *= a.pool.kv_heads;
-  const long long share = max(1LL + p.item_cost, (total + gridDim.x - 1) / gridDim.x);
-  const long long u0 = share * blockIdx.x, u1 = min(total, u0 + share);
-  if (u0 < u1) {
-    __syncthreads();                     // scan is used again
-    // the sequence of place u0: chunks of 16 sequences, one a warp
-    long long base = 0;
-    for (int b0 = 0; b0 < a.seqs.batch; b0 += kThreads / 32) {
-      const long long c = seq_cost(b0 + warp) * a.pool.kv_heads;
-      if (lane == 0) sm.scan[warp] = c;
-      __syncthreads();
-      long long run = base;
-      int found = -1;
-      for (int w = 0; w < kThreads / 32 && found < 0; ++w) {
-        if (u0 < run + sm.scan[w]) found = w;
-        else run += sm.scan[w];
-      }
-      if (found >= 0) {
-        if (warp == found) {             // the head, then the pair of rows, in it
-          Seq s;
-          load_seq(a.seqs, b0 + warp, a.q.rows, &s);
-          const long long per = c / a.pool.kv_heads;
-          const int h = (int)((u0 - run) / per);
-          run += h * per;
-          for (int i0 = 0;; i0 += 32) {
-            const long long n = i0 + lane < pairs_of(a, s) ? item_of(a, s, i0 + lane, p.item_cost).cost : 0;
-            long long upto = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-              const long long up = __shfl_up_sync(FULL, upto, d);
-              if (lane >= d) upto += up;
-            }
-            const unsigned hit = __ballot_sync(FULL, run + upto > u0);
-            if (hit || i0 + 32 >= pairs_of(a, s)) {
-              if (lane == (hit ? __ffs(hit) - 1 : 0)) {
-                sm.start_b = b0 + warp;
-                sm.start_h = h;
-                sm.start_p = i0 + lane;
-                sm.before = run + upto - n;
-              }
-              break;
-            }
-            run += __shfl_sync(FULL, upto, 31);
-          }
-        }
-        break;
-      }
-      base = run;
-      __syncthreads();
-    }
-    __syncthreads();
-
-    Walk w;
-    const auto enter = [&]() {
-      w.it = item_of(a, w.s, w.p, p.item_cost);
-      w.t_begin = w.it.t0 + (int)min((long long)w.it.n, max(0LL, u0 - w.item0));
-      w.t_end = w.it.t0 + (int)min((long long)w.it.n, u1 - w.item0);
-    };
-    w.b = sm.start_b;
-    w.h = sm.start_h;
-    w.p = sm.start_p;
-    w.item0 = sm.before;
-    w.count = 0;
-    load_seq(a.seqs, w.b, a.q.rows, &w.s);
-    w.pairs = pairs_of(a, w.s);
-    enter();
-    // the next item of this block, false at its share's end
-    const auto next = [&]() -> bool {
-      w.item0 += w.it.cost;
-      if (w.item0 >= u1) return false;
-      if (++w.p == w.pairs) {
-        w.p = 0;
-        if (++w.h == a.pool.kv_heads) {
-          w.h = 0;
-          do {
-            if (!load_seq(a.seqs, ++w.b, a.q.rows, &w.s)) w.s.n = 0;
-            w.pairs = pairs_of(a, w.s);
-          } while (w.pairs == 0);        // the line goes on: there is one
-        }
-      }
-      enter();
-      return true;
-    };
-
+  Walk<kKeys, 2 * kRows> w;
+  if (w.template start<kThreads>(a, sm.walk, p.item_cost, 1 + p.item_cost)) {
     if (warp < 8) {
       // =========================== softmax and output ===========================
       const int slot = warp >> 2, r = threadIdx.x & (kRows - 1);
@@ -450,8 +322,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           tc_fence_after();
         }
         // ---- the rows' results: complete, or a part of an item that other blocks work on too ----
-        const int c0 = (int)(w.item0 / share), c1 = (int)((w.item0 + w.it.n - 1) / share);
-        const size_t part = (size_t)(2 * blockIdx.x + (w.item0 < u0 ? 0 : 1)) * 256;
+        const int c0 = w.first_block(), c1 = w.last_block();
+        const size_t part = (size_t)w.part() * 256;
         const auto out_row = [&](int i, int hh) {
           return a.o.data + w.b * a.o.seq + (long long)(w.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
         };
@@ -514,9 +386,9 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           tc_fence_before();             // O is read before the next item's first product overwrites it
         }
         // the block that begins an item which others go on with leaves word of it for the joining kernel
-        if (threadIdx.x == 0 && c0 != c1 && w.item0 >= u0) p.split[blockIdx.x] = make_int4(w.b, w.h, w.p, c1 - c0 + 1);
+        if (threadIdx.x == 0 && c0 != c1 && !w.began_before()) p.split[blockIdx.x] = make_int4(w.b, w.h, w.p, c1 - c0 + 1);
         ++w.count;
-      } while (next());
+      } while (w.next(a));
     } else if (warp < 12) {
       // =========================== values made ready ===========================
       const int r = threadIdx.x & 127;   // my key of the tile
@@ -619,7 +491,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           }
         }
         ++w.count;
-      } while (next());
+      } while (w.next(a));
     } else if (warp == 12) {
       // =============================== producer ===============================
       if (lane == 0) {
@@ -670,7 +542,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             }
           }
         }
-      } while (next());
+      } while (w.next(a));
       // every copy lands before this block's shared memory is released
       if (lane == 0)
         for (uint32_t i = n_tile > kStages ? n_tile - kStages : 0; i < n_tile; ++i) {
@@ -737,7 +609,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             }
           }
         }
-      } while (next());
+      } while (w.next(a));
       mma_commit(&sm.drain);
       mbar_drain(&sm.drain, 0, p.wait_ns);
     }

@@ -1,5 +1,5 @@
-// One query row over a run of cached keys by one warp, without tensor cores: the whole of the fp32
-// kernel, and what the tensor-core kernels fall back to for data their operands cannot hold.
+// One query row over a run of cached keys by one warp: what the tiled kernels fall back to for data
+// that their products cannot take (values that are not finite and not seen by all rows of a tile).
 #pragma once
 
 #include "cache.cuh"

@@ -1,0 +1,170 @@
+// How attention over the cache is shared out among the blocks of a launch.
+//
+// An item is up to kRows rows of one sequence and key/value head (rows: its new tokens times the group
+// of query heads, token by token), with the keys that any of them sees in tiles of kKeys.  All items
+// form one line, sequence by sequence, head by head; in it an item takes a place for each of its tiles
+// and then item_cost places for what it costs besides them.  The line is cut into equal shares, one a
+// block, so a block works on the end of one item, whole items, and the beginning of another, whatever
+// the lengths.  Everything is computed on the device, from the lengths there.
+#pragma once
+
+#include "cache.cuh"
+
+namespace pisa {
+namespace cache {
+
+template <int kWarps>
+struct WalkScratch {                  // in shared memory
+  long long scan[kWarps], before;
+  int b, h, p;
+};
+
+// Every role of a block walks its own copy.
+template <int kKeys, int kRows>
+struct Walk {
+  struct Item {
+    int t0, n, rows, first;           // its tiles are [t0, t0 + n) of the sequence; first: the first key any row sees
+    long long cost;
+  };
+  int b, h, p, pieces, count;         // sequence, head, piece of its rows (of `pieces`); count: for the caller's use
+  Seq s;
+  Item it;
+  long long item0, u0, u1, share;     // places: the item's first, this block's share, and how long shares are
+  int t_begin, t_end, item_cost;      // this block's tiles of the item: none where its share holds only the last places
+
+  static __device__ __forceinline__ int pieces_of(const AttnArgs& a, const Seq& s) { return (s.n * a.group + kRows - 1) / kRows; }
+  static __device__ __forceinline__ Item item_of(const AttnArgs& a, const Seq& s, int p, int item_cost) {
+    Item it;
+    it.rows = min(kRows, s.n * a.group - kRows * p);
+    int f0, l0, f1, l1;
+    const int pos = s.len - s.n;
+    visible(a, s.len, pos + kRows * p / a.group, &f0, &l0);
+    visible(a, s.len, pos + (kRows * p + it.rows - 1) / a.group, &f1, &l1);
+    // rows that see nothing (before the cache's first position) leave the range to the others
+    const int first = l0 > f0 ? f0 : 0, last = max(l0, l1);
+    it.first = first;
+    it.t0 = first / kKeys;
+    it.n = max(1, (last + kKeys - 1) / kKeys - it.t0);      // rows that see nothing are written too
+    it.cost = it.n + item_cost;
+    return it;
+  }
+
+  // Whole block of kThreads; false if the line ends before this block's share.
+  template <int kThreads, typename Scratch>
+  __device__ __forceinline__ bool start(const AttnArgs& a, Scratch& sc, int cost_of_item, int min_share) {
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    item_cost = cost_of_item;
+    // places of a sequence and head: a warp a sequence, lanes over its pieces
+    const auto seq_cost = [&](int b) -> long long {
+      Seq s;
+      long long c = 0;
+      if (b < a.seqs.batch && load_seq(a.seqs, b, a.q.rows, &s))
+        for (int i = lane; i < pieces_of(a, s); i += 32) c += item_of(a, s, i, item_cost).cost;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+      return c;
+    };
+    long long mine = 0;
+    for (int b = warp; b < a.seqs.batch; b += kWarps) mine += seq_cost(b);
+    if (lane == 0) sc.scan[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += sc.scan[w];
+    total *= a.pool.kv_heads;
+    share = max((long long)min_share, (total + gridDim.x - 1) / gridDim.x);
+    u0 = share * blockIdx.x;
+    u1 = min(total, u0 + share);
+    if (u0 >= u1) return false;
+    __syncthreads();                  // scan is used again
+    long long base = 0;
+    for (int b0 = 0; b0 < a.seqs.batch; b0 += kWarps) {
+      const long long c = seq_cost(b0 + warp) * a.pool.kv_heads;
+      if (lane == 0) sc.scan[warp] = c;
+      __syncthreads();
+      long long run = base;
+      int found = -1;
+      for (int w = 0; w < kWarps && found < 0; ++w) {
+        if (u0 < run + sc.scan[w]) found = w;
+        else run += sc.scan[w];
+      }
+      if (found >= 0) {
+        if (warp == found) {          // the head, then the piece of rows, in it
+          Seq s;
+          load_seq(a.seqs, b0 + warp, a.q.rows, &s);
+          const long long per = c / a.pool.kv_heads;
+          const int h = (int)((u0 - run) / per);
+          run += h * per;
+          for (int i0 = 0;; i0 += 32) {
+            const long long n = i0 + lane < pieces_of(a, s) ? item_of(a, s, i0 + lane, item_cost).cost : 0;
+            long long upto = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const long long up = __shfl_up_sync(0xffffffffu, upto, d);
+              if (lane >= d) upto += up;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, run + upto > u0);
+            if (hit || i0 + 32 >= pieces_of(a, s)) {
+              if (lane == (hit ? __ffs(hit) - 1 : 0)) {
+                sc.b = b0 + warp;
+                sc.h = h;
+                sc.p = i0 + lane;
+                sc.before = run + upto - n;
+              }
+              break;
+            }
+            run += __shfl_sync(0xffffffffu, upto, 31);
+          }
+        }
+        break;
+      }
+      base = run;
+      __syncthreads();
+    }
+    __syncthreads();
+    b = sc.b;
+    h = sc.h;
+    p = sc.p;
+    item0 = sc.before;
+    count = 0;
+    load_seq(a.seqs, b, a.q.rows, &s);
+    pieces = pieces_of(a, s);
+    enter(a);
+    return true;
+  }
+
+  __device__ __forceinline__ void enter(const AttnArgs& a) {
+    it = item_of(a, s, p, item_cost);
+    t_begin = it.t0 + (int)min((long long)it.n, max(0LL, u0 - item0));
+    t_end = it.t0 + (int)min((long long)it.n, u1 - item0);
+  }
+
+  // The next item of this block, false at its share's end.
+  __device__ __forceinline__ bool next(const AttnArgs& a) {
+    item0 += it.cost;
+    if (item0 >= u1) return false;
+    if (++p == pieces) {
+      p = 0;
+      if (++h == a.pool.kv_heads) {
+        h = 0;
+        do {
+          if (!load_seq(a.seqs, ++b, a.q.rows, &s)) s.n = 0;
+          pieces = pieces_of(a, s);
+        } while (pieces == 0);        // the line goes on: there is one
+      }
+    }
+    enter(a);
+    return true;
+  }
+
+  // Blocks that work on the item; a block has at most two items that it shares: the one that began before its
+  // share (part 2 * block) and the one that goes on after it (part 2 * block + 1).
+  __device__ __forceinline__ int first_block() const { return (int)(item0 / share); }
+  __device__ __forceinline__ int last_block() const { return (int)((item0 + it.n - 1) / share); }
+  __device__ __forceinline__ bool began_before() const { return item0 < u0; }
+  __device__ __forceinline__ int part() const { return 2 * blockIdx.x + (began_before() ? 0 : 1); }
+};
+
+}  // namespace cache
+}  // namespace pisa
