@@ -20,11 +20,11 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 64;
 constexpr unsigned FULL = 0xffffffffu;
 
 template <int D, int kRI>
 struct alignas(16) Smem {
+  static constexpr int kKeys = D == 128 ? 32 : 64;          // two blocks fit an SM
   static constexpr int kRows = 16 * kRI, kLd = D + 4;       // padded: 8 rows' float4 fall on all banks
   float q[kRows][kLd];
   float k[2][kKeys][kLd];
@@ -32,7 +32,8 @@ struct alignas(16) Smem {
   float s[kRows][kKeys + 4];
   float f[kRows];                       // what O is scaled by before a tile's products
   float m[kRows], l[kRows];
-  uint32_t bad[2][2];                   // keys of a tile whose page is missing
+  uint32_t bad[2][kKeys / 32];                   // keys of a tile whose page is missing
+  uint8_t bad4[2][8];                   // the same, four keys a byte
   WalkScratch<kThreads / 32> walk;
   int last;
 };
@@ -51,9 +52,11 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int D, int kRI>
-__global__ void __launch_bounds__(kThreads) attn_fp32(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_fp32(const Params p) {
   using S = Smem<D, kRI>;
-  constexpr int kRows = S::kRows, kCols = D / 64;           // float4 columns of O a thread
+  constexpr int kRows = S::kRows, kKeys = S::kKeys;
+  constexpr int kCols = D / 64, kKJ = kKeys / 16;           // a thread: float4 columns of O, keys of a row's scores
+  constexpr int kQuads = kThreads / kKeys;                  // threads that load a key
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const AttnArgs& a = p.a;
@@ -62,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) attn_fp32(const Params p) {
   if (!w.template start<kThreads>(a, sm.walk, 2, 1)) return;
   // products: rows rx + 16 i, keys kx + 16 j, columns 4 (kx) + 64 j
   const int rx = (lane >> 3) + 4 * (warp & 3), kx = (lane & 7) + 8 * (warp >> 2);
-  // softmax: four threads a row, 16 keys each (kRows * 4 threads)
+  // softmax: four threads a row (kRows * 4 threads)
   const int sr = tid >> 2, sq = tid & 3;
   const bool soft = sr < kRows;
 
@@ -70,30 +73,38 @@ __global__ void __launch_bounds__(kThreads) attn_fp32(const Params p) {
     if (w.t_begin >= w.t_end) continue;
     const int rows = w.it.rows;
     __syncthreads();                                        // the item before is done with shared memory
-    // a thread a key and quarter of its row: page by page, two tiles deep
+    // kQuads threads a key.  The page of a tile's key is looked up a tile ahead of its loads.
+    const int key_l = tid / kQuads;
+    int page = -1;
+    const auto look_up = [&](int t) {
+      const int j = t * kKeys + key_l;
+      page = t < w.t_end && j < w.s.len && j >= w.it.first ? load_page(a.seqs, a.pool, w.b, j) : -1;
+    };
     const auto load_tile = [&](int t) {
-      const int buf = t & 1, key = tid >> 2, j = t * kKeys + key;
-      int slot = -1;
-      if (j < w.s.len && j >= w.it.first) {
-        const int pg = load_page(a.seqs, a.pool, w.b, j);
-        if (pg >= 0) slot = (pg * a.pool.kv_heads + w.h) * a.pool.page + (j & (a.pool.page - 1));
-      }
-      const float* ks = reinterpret_cast<const float*>(a.pool.k) + (size_t)max(slot, 0) * D;
-      const float* vs = reinterpret_cast<const float*>(a.pool.v) + (size_t)max(slot, 0) * D;
+      const int buf = t & 1, j = t * kKeys + key_l;
+      const bool there = page >= 0;
+      const size_t slot = there ? (size_t)((page * a.pool.kv_heads + w.h) * a.pool.page + (j & (a.pool.page - 1))) : 0;
+      const float* ks = reinterpret_cast<const float*>(a.pool.k) + slot * D;
+      const float* vs = reinterpret_cast<const float*>(a.pool.v) + slot * D;
 #pragma unroll
-      for (int c = tid & 3; c < D / 4; c += 4) {
-        cp16(&sm.k[buf][key][4 * c], ks + 4 * c, slot >= 0);      // zeros where there is no key
-        cp16(&sm.v[buf][key][4 * c], vs + 4 * c, slot >= 0);
+      for (int x = 0; x < D / 4 / kQuads; ++x) {
+        const int c = tid % kQuads + x * kQuads;
+        cp16(&sm.k[buf][key_l][4 * c], ks + 4 * c, there);        // zeros where there is no key
+        cp16(&sm.v[buf][key_l][4 * c], vs + 4 * c, there);
       }
       cp_commit();
-      // 8 keys a warp: bits of the missing ones
-      const unsigned miss = __ballot_sync(FULL, slot < 0);
+      // a warp's 32 / kQuads keys: bits of the missing ones
+      const unsigned miss = __ballot_sync(FULL, !there);
       if (lane == 0) {
         uint32_t bits = 0;
-        for (int x = 0; x < 8; ++x) bits |= ((miss >> (4 * x)) & 1u) << x;
-        reinterpret_cast<uint8_t*>(sm.bad[buf])[warp] = (uint8_t)bits;
+#pragma unroll
+        for (int x = 0; x < 32 / kQuads; ++x) bits |= ((miss >> (kQuads * x)) & 1u) << x;
+        if (kQuads == 4) reinterpret_cast<uint8_t*>(sm.bad[buf])[warp] = (uint8_t)bits;
+        else sm.bad4[buf][warp] = (uint8_t)bits;
       }
+      look_up(t + 1);
     };
+    look_up(w.t_begin);
     load_tile(w.t_begin);
     for (int e = tid; e < kRows * (D / 4); e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4);
@@ -143,22 +154,22 @@ __global__ void __launch_bounds__(kThreads) attn_fp32(const Params p) {
         odd = __syncthreads_or(here) || odd;
       }
       // ---- scores ----
-      uint64_t acc[kRI][4];
+      uint64_t acc[kRI][kKJ];
 #pragma unroll
       for (int i = 0; i < kRI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
+        for (int j = 0; j < kKJ; ++j) acc[i][j] = 0ull;
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        ulonglong2 qv[kRI], kv[4];
+        ulonglong2 qv[kRI], kv[kKJ];
 #pragma unroll
         for (int i = 0; i < kRI; ++i) qv[i] = *reinterpret_cast<const ulonglong2*>(&sm.q[rx + 16 * i][d]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(&sm.k[buf][kx + 16 * j][d]);
+        for (int j = 0; j < kKJ; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(&sm.k[buf][kx + 16 * j][d]);
 #pragma unroll
         for (int i = 0; i < kRI; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < kKJ; ++j) {
             acc[i][j] = f2_fma(qv[i].x, kv[j].x, acc[i][j]);
             acc[i][j] = f2_fma(qv[i].y, kv[j].y, acc[i][j]);
           }
@@ -166,19 +177,28 @@ __global__ void __launch_bounds__(kThreads) attn_fp32(const Params p) {
 #pragma unroll
       for (int i = 0; i < kRI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kKJ; ++j) {
           float x, y;
           f2_unpack(acc[i][j], x, y);
           sm.s[rx + 16 * i][kx + 16 * j] = (x + y) * a.scale_log2;
         }
       __syncthreads();
-      // ---- weights: my 16 keys are sq, sq + 4, ... ----
+      // ---- weights: my keys are sq, sq + 4, ... ----
       if (soft) {
-        const uint32_t* bad = sm.bad[buf];
-        float x[16], mx = -INFINITY;
-        const bool care = j0 < af || j0 + kKeys > al || (bad[0] | bad[1]);
+        uint32_t bad[kKeys / 32];
+        if (kQuads == 4) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < kKeys / 32; ++e) bad[e] = sm.bad[buf][e];
+        } else {
+          bad[0] = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) bad[0] |= (uint32_t)sm.bad4[buf][e] << (4 * e);
+        }
+        constexpr int kMine = kKeys / 4;
+        float x[kMine], mx = -INFINITY;
+        const bool care = j0 < af || j0 + kKeys > al || (bad[0] | bad[kKeys / 32 - 1]);
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
           const int key = sq + 4 * e;
           x[e] = sm.s[sr][key];
           if (care && (j0 + key < first || j0 + key >= last || ((bad[key >> 5] >> (key & 31)) & 1u))) x[e] = -INFINITY;
@@ -190,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) attn_fp32(const Params p) {
         const float f = exp2f(m - base);                    // 0 when m = -inf
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < kMine; ++e) {
           x[e] = exp2f(x[e] - base);
           sum += x[e];
           sm.s[sr][sq + 4 * e] = x[e];
