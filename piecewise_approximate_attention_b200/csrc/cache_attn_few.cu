@@ -38,10 +38,15 @@ namespace cache {
 namespace {
 using namespace sm100;
 
-constexpr int kTile = 64;                    // keys
 constexpr int kConsumers = 128;
 constexpr int kThreads = kConsumers + 32;
 constexpr float kLazyLog2 = 8.f;
+#ifndef ITEM_COST
+#define ITEM_COST (esz == 1 ? 3 : 1)
+#endif
+#ifndef MIN_SHARE
+#define MIN_SHARE 2
+#endif
 constexpr unsigned FULL = 0xffffffffu;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
@@ -71,10 +76,11 @@ __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;
 
 template <int D, bool kF8>
 struct Layout {
+  static constexpr int kTile = kF8 ? 128 : 64;                    // keys: the same bytes either way
   static constexpr int kRowBytes = kF8 ? D : 128;                 // of a swizzled tile's row
   static constexpr int kHalves = kF8 ? 1 : D / 64;                // 64-column bf16 halves
   static constexpr int kSide = kTile * D * (kF8 ? 1 : 2);         // bytes of a K or V tile
-  static constexpr int kStages = kF8 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+  static constexpr int kStages = D == 128 ? 3 : 6;
 };
 
 template <int D, bool kF8>
@@ -82,12 +88,12 @@ struct alignas(1024) Smem {
   using L = Layout<D, kF8>;
   uint8_t k[L::kStages][L::kSide];
   uint8_t v[L::kStages][L::kSide];
-  uint8_t ke[L::kStages][kF8 ? kTile : 16];
-  uint8_t ve[L::kStages][kF8 ? kTile : 16];
+  uint8_t ke[L::kStages][kF8 ? L::kTile : 16];
+  uint8_t ve[L::kStages][kF8 ? L::kTile : 16];
   uint64_t full[L::kStages], empty[L::kStages];
-  unsigned long long bad[L::kStages];        // keys of the tile whose page is no page of the pool, or is not there
+  unsigned long long bad[L::kStages][L::kTile / 64];      // keys of the tile whose page is no page of the pool, or is not there
   long long scan[kThreads / 32], before;
-  float2 ml[2][16];                          // maximum and sum of the rows that a warp hands over
+  float2 ml[4][16];                          // maximum and sum of the rows that a warp hands over
   int start_b, abort, last;
 };
 
@@ -107,6 +113,7 @@ struct Item {
   int t0, n, first;             // first: the first key that any row sees
   long long cost;
 };
+template <int kTile>
 __device__ __forceinline__ Item load_item(const AttnArgs& a, int b, int item_cost) {
   Item it;
   it.t0 = it.n = it.first = 0;
@@ -134,7 +141,7 @@ __device__ __forceinline__ void wait(S& sm, uint64_t* bar, uint32_t parity, cons
 template <int D, bool kF8>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   if (kF8) return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  return (c >> 3) * (64 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // Element (row r, column c) of a V tile.
@@ -147,148 +154,624 @@ __device__ __forceinline__ float value_at(const uint8_t* tile, int r, int c) {
   return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(tile + chunk_at<D, false>(r, c >> 3) + 2 * (c & 7)));
 }
 
-template <int D, bool kF8, int MT>
-__global__ void __launch_bounds__(kThreads, 2)
-attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
-  using L = Layout<D, kF8>;
-  constexpr int kStages = L::kStages;
-  constexpr int kKeyGroups = 4 / MT, kSteps = 4 / kKeyGroups;     // 16-key steps of a warp in a tile
-  extern __shared__ uint8_t smem_raw[];
-  Smem<D, kF8>& sm = *reinterpret_cast<Smem<D, kF8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const AttnArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// a / b, by 32 bits where they do.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 
-  // ---- this block's share of the line of tiles ----
+// A block's share of the line, and where it is in it; every warp walks its own copy.
+template <int kTile>
+struct FewWalk {
+  long long u0, u1, share, item0;     // places: this block's, how long shares are, the item's first
+  int b, h, t_begin, t_end, item_cost;
+  Item it;
+
+  // Whole block; false if the line ends before this block's share.
+  template <typename S>
+  __device__ __forceinline__ bool start(const AttnArgs& a, S& sm, int cost_of_item, int min_share) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    item_cost = cost_of_item;
+    const auto places = [&](int b) { return b < a.seqs.batch ? load_item<kTile>(a, b, item_cost).cost * a.pool.kv_heads : 0LL; };
+    const auto scan = [&](long long n) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long up = __shfl_up_sync(FULL, n, d);
+        if (lane >= d) n += up;
+      }
+      return n;
+    };
+    long long total = 0, before = 0;
+    if (a.seqs.batch <= 32) {         // each warp by itself
+      const long long n = places(lane), upto = scan(n);
+      total = __shfl_sync(FULL, upto, 31);
+      shares(total, min_share);
+      if (u0 >= u1) return false;
+      const int w = __ffs(__ballot_sync(FULL, upto > u0)) - 1;
+      b = w;
+      before = __shfl_sync(FULL, upto - n, w);
+    } else {
+      for (int i = threadIdx.x; i < a.seqs.batch; i += kThreads) total += places(i);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(FULL, total, d);
+      if (lane == 0) sm.scan[warp] = total;
+      __syncthreads();
+      total = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) total += sm.scan[w];
+      shares(total, min_share);
+      if (u0 >= u1) return false;
+      if (warp == 0) {                // 32 sequences at a time
+        long long base = 0;
+        for (int b0 = 0; b0 < a.seqs.batch; b0 += 32) {
+          const long long n = places(b0 + lane), upto = scan(n);
+          const unsigned hit = __ballot_sync(FULL, base + upto > u0);
+          if (hit) {
+            const int w = __ffs(hit) - 1;
+            if (lane == w) {
+              sm.start_b = b0 + w;
+              sm.before = base + upto - n;
+            }
+            break;
+          }
+          base += __shfl_sync(FULL, upto, 31);
+        }
+      }
+      __syncthreads();
+      b = sm.start_b;
+      before = sm.before;
+    }
+    it = load_item<kTile>(a, b, item_cost);
+    h = (int)quotient(u0 - before, it.cost);
+    item0 = before + h * it.cost;
+    enter();
+    return true;
+  }
+  __device__ __forceinline__ void shares(long long total, int min_share) {
+    share = max((long long)min_share, quotient(total + gridDim.x - 1, gridDim.x));
+    u0 = share * blockIdx.x;
+    u1 = min(total, u0 + share);
+  }
+  // the tiles of the item that are this block's: none where its share holds only the item's last places
+  __device__ __forceinline__ void enter() {
+    t_begin = it.t0 + (int)min((long long)it.n, max(0LL, u0 - item0));
+    t_end = it.t0 + (int)min((long long)it.n, u1 - item0);
+  }
+  __device__ __forceinline__ bool next(const AttnArgs& a) {
+    item0 += it.cost;
+    if (item0 >= u1) return false;
+    if (++h == a.pool.kv_heads) {
+      h = 0;
+      do it = load_item<kTile>(a, ++b, item_cost); while (it.n == 0);   // the line goes on: there is one
+    }
+    enter();
+    return true;
+  }
+  // Blocks that work on the item, and this block's part of it: the end (2 * block) or the beginning (+ 1).
+  __device__ __forceinline__ int first_block() const { return (int)quotient(item0, share); }
+  __device__ __forceinline__ int last_block() const { return (int)quotient(item0 + it.n - 1, share); }
+  __device__ __forceinline__ size_t part() const { return (size_t)(2 * blockIdx.x + (item0 < u0 ? 0 : 1)) * kMaxFewRows; }
+};
+__device__ __forceinline__ size_t part_of(int block, int first) { return (size_t)(2 * block + (block == first)) * kMaxFewRows; }
+
+// The producer warp: follows the page table and fills the ring.  kJoin: a stage after each item's tiles
+// is left to the consumers, to join their results in.
+template <int D, bool kF8, bool kJoin, typename S>
+__device__ __forceinline__ void produce(S& sm, const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p,
+                                        FewWalk<Layout<D, kF8>::kTile>& w) {
+  using L = Layout<D, kF8>;
+  constexpr int kTile = L::kTile, kStages = L::kStages;
+  const AttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  const int box = min(a.pool.page, kTile), log_box = min(a.pool.page_log2, kF8 ? 7 : 6), pages = kTile >> log_box;   // boxes of a tile
+  constexpr int per = 2 * L::kHalves;                                  // copies of a box
+  const uint32_t box_bytes = 2u * box * D * (kF8 ? 1 : 2) + (kF8 ? 2u * box : 0u);
+  int ring = 0;                                                        // stages used so far
+  do {
+    for (int t = w.t_begin; t < w.t_end; ++t, ++ring) {
+      const int st = ring % kStages;
+      // lane i < pages looks box i's page up
+      int row = -1;
+      const int pos = t * kTile + lane * box;
+      if (lane < pages && pos < w.it.s.len && pos + box > w.it.first) {
+        const int pg = load_page(a.seqs, a.pool, w.b, pos);
+        if (pg >= 0) row = (pg * a.pool.kv_heads + w.h) * a.pool.page + (pos & (a.pool.page - 1));
+      }
+      if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
+      const unsigned have = __ballot_sync(FULL, row >= 0);
+      if (lane < kTile / 64) {
+        unsigned long long bits = 0;
+        for (int i = 0; i < 64; i += 16)
+          if (!((have >> ((lane * 64 + i) >> log_box)) & 1u)) bits |= 0xffffull << i;
+        sm.bad[st][lane] = bits;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_expect_tx(&sm.full[st], __popc(have) * box_bytes);
+      __syncwarp();
+      // copies (box, K or V, half) over the lanes: at most 32
+      const int i = lane / per, side = lane % per & 1, half = lane % per >> 1;
+      const int r = __shfl_sync(FULL, row, i);
+      if (i < pages && r >= 0) {
+        uint8_t* dst = (side ? sm.v[st] : sm.k[st]) + half * (kTile * 128) + i * box * L::kRowBytes;
+        tma_load_3d(dst, side ? &vmap : &kmap, &sm.full[st], half * 64, r, 0);
+        if (kF8) bulk_load((side ? sm.ve[st] : sm.ke[st]) + i * box, (side ? a.pool.v_exp : a.pool.k_exp) + r, box, &sm.full[st]);
+      }
+    }
+    if (kJoin && w.t_begin < w.t_end) {
+      const int st = ring % kStages;
+      if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
+      if (lane == 0) mbar_arrive(&sm.full[st]);
+      ++ring;
+    }
+  } while (w.next(a));
+  // every copy lands before this block's shared memory is released
+  if (lane == 0)
+    for (int i = max(0, ring - kStages); i < ring; ++i) mbar_drain(&sm.full[i % kStages], (i / kStages) & 1, p.wait_ns);
+}
+
+// Barriers, and whether the block has a share.
+template <int D, bool kF8, typename S>
+__device__ __forceinline__ bool set_up(S& sm, const Params& p, FewWalk<Layout<D, kF8>::kTile>& w) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < Layout<D, kF8>::kStages; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 4);
     }
     sm.abort = 0;
     fence_mbar_init();
   }
-  long long mine = 0;
-  for (int b = threadIdx.x; b < a.seqs.batch; b += kThreads) mine += load_item(a, b, p.item_cost).cost * a.pool.kv_heads;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(FULL, mine, d);
-  if (lane == 0) sm.scan[warp] = mine;
+  const bool any = w.start(p.a, sm, p.item_cost, p.min_share);
   __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) total += sm.scan[w];
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < p.min_share) share = p.min_share;
-  const long long u0 = share * blockIdx.x, u1 = min(total, u0 + share);
-  if (u0 >= u1) return;
-  // the sequence that tile u0 belongs to, and the tiles before it: warp 0 scans 32 sequences at a time
-  if (warp == 0) {
-    long long base = 0;
-    for (int b0 = 0; b0 < a.seqs.batch; b0 += 32) {
-      const long long n = b0 + lane < a.seqs.batch ? load_item(a, b0 + lane, p.item_cost).cost * a.pool.kv_heads : 0;
-      long long run = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long up = __shfl_up_sync(FULL, run, d);
-        if (lane >= d) run += up;
-      }
-      const unsigned hit = __ballot_sync(FULL, base + run > u0);
-      if (hit) {
-        const int w = __ffs(hit) - 1;
-        if (lane == w) {
-          sm.start_b = b0 + w;
-          sm.before = base + run - n;
-        }
-        break;
-      }
-      base += __shfl_sync(FULL, run, 31);
-    }
+  return any;
+}
+
+// The block that ends last joins the parts of an item, in the order of the blocks: 16 threads a row of
+// eight, or kLanes16 = false: D / 4 threads a row.  Consumer warps only; true in that block's threads.
+template <typename S>
+__device__ __forceinline__ bool ends_last(S& sm, const Params& p, int c0, int c1) {
+  __threadfence();
+  consumer_sync();
+  if (threadIdx.x == 0) {
+    const bool done = atomicAdd(p.counters + c0, 1) == c1 - c0;
+    if (done) p.counters[c0] = 0;                            // as the next call finds it
+    sm.last = done;
   }
-  __syncthreads();
-
-  int b = sm.start_b;
-  Item it = load_item(a, b, p.item_cost);
-  int h = (int)((u0 - sm.before) / it.cost);
-  long long item0 = sm.before + h * it.cost;                  // the item's first place in the line
-  int ring = 0;                                               // stages used so far
-  const auto next_item = [&]() {
-    item0 += it.cost;
-    if (++h == a.pool.kv_heads) {
-      h = 0;
-      do it = load_item(a, ++b, p.item_cost); while (it.n == 0);   // the line goes on: there is one
+  consumer_sync();
+  const bool last = sm.last;
+  if (last) __threadfence();
+  return last;
+}
+template <int D>
+__device__ __forceinline__ void join_parts(const Params& p, const Item& it, int b, int h, int c0, int c1) {
+  constexpr int kLanes = D / 8;                              // threads a row, eight columns each
+  const AttnArgs& a = p.a;
+  const int x = threadIdx.x % kLanes, rows = it.s.n * a.group, parts = c1 - c0 + 1;
+  // uniform trips: the shuffles take whole warps
+  for (int r0 = 0; r0 < rows; r0 += kConsumers / kLanes) {
+    const int r = r0 + threadIdx.x / kLanes, rr = min(r, rows - 1);
+    float m = -INFINITY, l = 0.f;
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int y0 = 0; y0 < parts; y0 += kLanes) {             // lane x: part y0 + x
+      const float2 ml = y0 + x < parts ? __ldcg(&p.part_ml[part_of(c0 + y0 + x, c0) + rr]) : make_float2(-INFINITY, 0.f);
+      float mx = ml.x;
+#pragma unroll
+      for (int d = kLanes / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d, kLanes));
+      const float m_new = fmaxf(m, mx), base = m_new == -INFINITY ? 0.f : m_new;
+      const float f0 = ex2(m - base), fx = ex2(ml.x - base);
+      float sum = ml.y * fx;
+#pragma unroll
+      for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d, kLanes);
+      l = l * f0 + sum;
+      m = m_new;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) o[e] = make_float4(o[e].x * f0, o[e].y * f0, o[e].z * f0, o[e].w * f0);
+#pragma unroll 4
+      for (int y = 0; y < min(kLanes, parts - y0); ++y) {
+        const float f = __shfl_sync(FULL, fx, y, kLanes);
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (part_of(c0 + y0 + y, c0) + rr) * D) + 2 * x;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 v = __ldcg(src + e);
+          o[e].x = fmaf(v.x, f, o[e].x);
+          o[e].y = fmaf(v.y, f, o[e].y);
+          o[e].z = fmaf(v.z, f, o[e].z);
+          o[e].w = fmaf(v.w, f, o[e].w);
+        }
+      }
     }
-  };
-  // the tiles of the item that are this block's: [t_begin, t_end), none where its share holds only the item's last places
-  const auto tiles = [&](int* t_begin, int* t_end) {
-    *t_begin = it.t0 + (int)min((long long)it.n, max(0LL, u0 - item0));
-    *t_end = it.t0 + (int)min((long long)it.n, u1 - item0);
-  };
+    if (r >= rows) continue;
+    const int i = r / a.group, hh = h * a.group + r - i * a.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
+    *reinterpret_cast<uint4*>(dst + x * 16) = make_uint4(pack_bf16x2(o[0].x * inv, o[0].y * inv), pack_bf16x2(o[0].z * inv, o[0].w * inv),
+                                                        pack_bf16x2(o[1].x * inv, o[1].y * inv), pack_bf16x2(o[1].z * inv, o[1].w * inv));
+    float* lse = lse_at(a, b, it.s, i, hh);
+    if (lse && x == 0) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// At most 8 rows: the keys are the 16 rows of the MMA's A operand and the queries its 8 columns, which
+// takes half the instructions and half the accumulators of the form below.  S^T = K Q^T, O^T += V^T P^T;
+// P^T is turned from the scores' layout to the operand's by movmatrix.  Each warp takes kTile / 4 keys
+// of a tile.  The warps' O meet in a stage of the ring, 16 threads finish a row.
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kThreads, 2)
+attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
+  using L = Layout<D, kF8>;
+  constexpr int kStages = L::kStages, kTile = L::kTile, kSub = kTile / 64;     // 16-key pieces of a warp's keys
+  extern __shared__ uint8_t smem_raw[];
+  Smem<D, kF8>& sm = *reinterpret_cast<Smem<D, kF8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  FewWalk<kTile> wk;
+  if (!set_up<D, kF8>(sm, p, wk)) return;
   if (warp == 4) {
-    // =============================== producer ===============================
-    if (lane == 0) {
-      tma_prefetch_desc(&kmap);
-      tma_prefetch_desc(&vmap);
+    produce<D, kF8, true>(sm, kmap, vmap, p, wk);
+    return;
+  }
+  const int g = lane >> 2, q4 = lane & 3;
+  int ring = 0;                                               // stages used so far
+  do {
+    if (wk.t_begin >= wk.t_end) continue;
+    const Item& it = wk.it;
+    const int b = wk.b, h = wk.h, rows = it.s.n * a.group;
+    // query row g into the B fragments
+    uint32_t qb[D / 16][2];
+    float rs_g = a.scale_log2;                                // raw score -> base-2 logit
+    {
+      const char* src = nullptr;
+      if (g < rows) {
+        const int i = g / a.group, hh = h * a.group + g - i * a.group;
+        src = a.q.data + b * a.q.seq + (long long)(it.s.row0 + i) * a.q.row + (long long)hh * a.q.head;
+      }
+      if constexpr (kF8) {
+        // K fragments hold codes 4 q4 ... 4 q4 + 3 of a 16-code chunk as their k positions 2 q4, 2 q4 + 1 and +8
+        uint2 x[D / 16];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          x[c] = src ? *reinterpret_cast<const uint2*>(src + c * 32 + q4 * 8) : make_uint2(0, 0);
+          mx = max(mx, max(max((x[c].x << 16) & 0x7fff0000u, x[c].x & 0x7fff0000u),
+                           max((x[c].y << 16) & 0x7fff0000u, x[c].y & 0x7fff0000u)));
+        }
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+        // largest magnitude to [2^14, 2^15): every bf16 down to 2^-31 of it is an fp16 number
+        const int eq = max(-100, min(112, (int)(mx >> 23) - 127 - 14));
+        const float s = pow2(-eq);
+        rs_g *= pow2(eq);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          qb[c][0] = pack_f16x2(__uint_as_float(x[c].x << 16) * s, __uint_as_float(x[c].x & 0xffff0000u) * s);
+          qb[c][1] = pack_f16x2(__uint_as_float(x[c].y << 16) * s, __uint_as_float(x[c].y & 0xffff0000u) * s);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          qb[c][0] = src ? *reinterpret_cast<const uint32_t*>(src + c * 32 + q4 * 4) : 0u;
+          qb[c][1] = src ? *reinterpret_cast<const uint32_t*>(src + c * 32 + 16 + q4 * 4) : 0u;
+        }
+      }
     }
-    const int box = min(a.pool.page, kTile), pages = kTile / box;      // boxes of a tile
-    const int per = 2 * L::kHalves;                                    // copies of a box
-    const uint32_t box_bytes = 2u * box * D * (kF8 ? 1 : 2) + (kF8 ? 2u * box : 0u);
-    for (;;) {
-      int t_begin, t_end;
-      tiles(&t_begin, &t_end);
-      for (int t = t_begin; t < t_end; ++t, ++ring) {
-        const int st = ring % kStages;
-        if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
-        // lane i < pages looks box i's page up
-        int row = -1;
-        const int pos = t * kTile + lane * box;
-        if (lane < pages && pos < it.s.len && pos + box > it.first) {
-          const int pg = load_page(a.seqs, a.pool, b, pos);
-          if (pg >= 0) row = (pg * a.pool.kv_heads + h) * a.pool.page + (pos & (a.pool.page - 1));
-        }
-        const unsigned have = __ballot_sync(FULL, row >= 0);
-        unsigned long long bad = 0;
-        for (int i = 0; i < pages; ++i)
-          if (!((have >> i) & 1u)) bad |= (box == 64 ? ~0ull : ((1ull << box) - 1ull)) << (i * box);
-        if (lane == 0) {
-          sm.bad[st] = bad;
-          mbar_expect_tx(&sm.full[st], __popc(have) * box_bytes);
-        }
-        __syncwarp();
-        // copies (box, K or V, half) over the lanes
-        for (int c = lane; c < ((pages * per + 31) & ~31); c += 32) {
-          const int i = c / per, side = c % per & 1, half = c % per >> 1;
-          const int r = __shfl_sync(FULL, row, i < pages ? i : 0);
-          if (i < pages && r >= 0) {
-            uint8_t* dst = (side ? sm.v[st] : sm.k[st]) + half * (kTile * 128) + i * box * L::kRowBytes;
-            tma_load_3d(dst, side ? &vmap : &kmap, &sm.full[st], half * 64, r, 0);
-            if (kF8) bulk_load((side ? sm.ve[st] : sm.ke[st]) + i * box, (side ? a.pool.v_exp : a.pool.k_exp) + r, box, &sm.full[st]);
+    // rows 2 q4 and 2 q4 + 1: the columns of my scores
+    float rs[2];
+    int first[2], last[2], all_first = 0, all_last = it.s.len;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * q4 + e;
+      rs[e] = __shfl_sync(FULL, rs_g, r * 4);
+      first[e] = last[e] = 0;
+      if (r < rows) {
+        visible(a, it.s.len, it.s.len - it.s.n + r / a.group, &first[e], &last[e]);
+        all_first = max(all_first, first[e]);
+        all_last = min(all_last, last[e]);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {                         // keys that all rows see: only those tiles need no masks
+      all_first = max(all_first, __shfl_xor_sync(FULL, all_first, d));
+      all_last = min(all_last, __shfl_xor_sync(FULL, all_last, d));
+    }
+    float acc[D / 16][4];                                     // rows 2 q4, 2 q4 + 1 of two columns (d_of)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+    const auto d_of = [&](int c, int e) { return kF8 ? 16 * c + 2 * g + e : 16 * c + g + 8 * e; };
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (int t = wk.t_begin; t < wk.t_end; ++t, ++ring) {
+      const int st = ring % kStages;
+      wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+      const uint32_t kb = smem_u32(sm.k[st]), vb = smem_u32(sm.v[st]);
+      const int k0 = warp * (kTile / 4), j0 = t * kTile + k0;
+      const unsigned bad_bits = (unsigned)(sm.bad[st][k0 >> 6] >> (k0 & 63)) & (kSub == 1 ? 0xffffu : FULL);
+      // this warp's keys of the tile; edge: some row does not see some of them
+      const auto keys = [&](auto edge_tag) {
+        constexpr bool edge = decltype(edge_tag)::value;
+        // ---- scores: keys g and g + 8 of each piece, rows 2 q4 and 2 q4 + 1 ----
+        float s[kSub][4] = {};
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            const int key = k0 + 16 * u + ((lane >> 3) & 1) * 8 + (lane & 7);
+            uint32_t x[4];
+            if constexpr (kF8) {
+              if (c & 1) continue;
+              ldsm4(kb + chunk_at<D, true>(key, c + (lane >> 4)), x);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t lo = x[2 * e], hi = x[2 * e + 1];
+                const uint32_t A[4] = {e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)hi),
+                                       e4m3x2_to_f16x2((uint16_t)(lo >> 16)), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
+                mma16816<true>(s[u], A, qb[c + e][0], qb[c + e][1]);
+              }
+            } else {
+              ldsm4(kb + chunk_at<D, false>(key, 2 * c + (lane >> 4)), x);
+              mma16816<false>(s[u], x, qb[c][0], qb[c][1]);
+            }
+          }
+        // ---- base-2 logits (e4m3: plus the exponent of the value's scale) ----
+        float inv[kSub][2];                                   // e4m3: 2^-e of my keys' values
+        unsigned seen[kSub];
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+          seen[u] = 0xfu;
+          if (edge) seen[u] = 0u;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int kk = 16 * u + 8 * x + g;
+            float ks = 1.f, ef = 0.f;
+            if (kF8) {
+              const uint32_t vx = sm.ve[st][k0 + kk];
+              ks = __uint_as_float((uint32_t)sm.ke[st][k0 + kk] << 23);
+              ef = (float)((int)vx - kExpBias);
+              inv[u][x] = __uint_as_float((254u - vx) << 23);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& y = s[u][2 * x + e];
+              y = kF8 ? fmaf(y * ks, rs[e], ef) : y * a.scale_log2;
+              if (edge) {
+                const int j = j0 + kk;
+                if (j >= first[e] && j < last[e] && !((bad_bits >> kk) & 1u)) seen[u] |= 1u << (2 * x + e);
+                else y = -INFINITY;
+              }
+              top[e] = fmaxf(top[e], y);
+            }
           }
         }
-      }
-      if (kKeyGroups > 1 && t_begin < t_end) {                // the stage that the key groups are joined through
-        const int st = ring % kStages;
-        if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
-        if (lane == 0) mbar_arrive(&sm.full[st]);
-        ++ring;
-      }
-      if (item0 + it.cost >= u1) break;
-      next_item();
+        // ---- running maximum: moved only when a row outgrows it by 2^8 ----
+        if (__any_sync(FULL, top[0] > m[0] + kLazyLog2 || top[1] > m[1] + kLazyLog2)) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(FULL, top[e], d));
+            const float mn = fmaxf(m[e], top[e]);
+            f[e] = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
+            m[e] = mn;
+            l[e] *= f[e];
+          }
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[c][x] *= f[x & 1];
+        }
+        const float mb[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        uint32_t pb[kSub][2];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& y = s[u][2 * x + e];
+              y = ex2(y - mb[e]);
+              if (kF8) {
+                if (!edge || ((seen[u] >> (2 * x + e)) & 1u)) l[e] = fmaf(y, inv[u][x], l[e]);
+              } else {
+                l[e] += y;
+              }
+            }
+            pb[u][x] = transpose8x8(kF8 ? pack_f16x2(s[u][2 * x], s[u][2 * x + 1]) : pack_bf16x2(s[u][2 * x], s[u][2 * x + 1]));
+          }
+        // ---- O^T += V^T P^T; A fragments hold keys 2 q4, 2 q4 + 1 and +8 ----
+        uint32_t keep[kSub][2];
+        if (edge) {
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              keep[u][n] = 0;
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int kk = 16 * u + 8 * n + 2 * q4 + x;
+                if (j0 + kk < it.s.len && !((bad_bits >> kk) & 1u)) keep[u][n] |= 0xffffu << (16 * x);
+              }
+            }
+        }
+        constexpr uint32_t kInf = kF8 ? 0x7c007c00u : 0x7f807f80u;
+        bool odd = false;                                     // a value that is not finite where not all rows see it
+        const auto clean = [&](uint32_t x, int u, int n) -> uint32_t {
+          if (!edge) return x;
+          x &= keep[u][n];
+          const bool lo = (x & kInf & 0xffffu) == (kInf & 0xffffu), hi = (x & kInf & 0xffff0000u) == (kInf & 0xffff0000u);
+          odd = odd || lo || hi;
+          if (lo) x &= 0xffff0000u;
+          if (hi) x &= 0x0000ffffu;
+          return x;
+        };
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t x[4];
+            if constexpr (kF8) {
+              if (c & 1) continue;
+              ldsm4t(vb + chunk_at<D, true>(k0 + 16 * u + ((lane >> 3) & 1) * 8 + (lane & 7), c + (lane >> 4)), x);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // bytes (key, d), (key, d + 1), (key + 1, d), (key + 1, d + 1) -> pairs of keys for d and for d + 1
+                const uint32_t lo = __byte_perm(x[2 * e], 0, 0x3120), hi = __byte_perm(x[2 * e + 1], 0, 0x3120);
+                const uint32_t A[4] = {clean(e4m3x2_to_f16x2((uint16_t)lo), u, 0), clean(e4m3x2_to_f16x2((uint16_t)(lo >> 16)), u, 0),
+                                       clean(e4m3x2_to_f16x2((uint16_t)hi), u, 1), clean(e4m3x2_to_f16x2((uint16_t)(hi >> 16)), u, 1)};
+                mma16816<true>(acc[c + e], A, pb[u][0], pb[u][1]);
+              }
+            } else {
+              ldsm4t(vb + chunk_at<D, false>(k0 + 16 * u + (lane >> 4) * 8 + (lane & 7), 2 * c + ((lane >> 3) & 1)), x);
+              const uint32_t A[4] = {clean(x[0], u, 0), clean(x[1], u, 0), clean(x[2], u, 1), clean(x[3], u, 1)};
+              mma16816<false>(acc[c], A, pb[u][0], pb[u][1]);
+            }
+          }
+        if (edge && __any_sync(FULL, odd)) {
+          // rare: add what was taken out, to the rows that see it
+#pragma unroll 1
+          for (int kk = 0; kk < 16 * kSub; ++kk) {
+            if (j0 + kk >= it.s.len || ((bad_bits >> kk) & 1u)) continue;
+            const int src = (kk & 7) * 4 + q4, x = (kk >> 3) & 1;
+            float wk2[2];
+            bool sk[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float y = 0.f;
+              unsigned z = 0;
+#pragma unroll
+              for (int u = 0; u < kSub; ++u)
+                if (u == kk >> 4) {
+                  y = x ? s[u][2 + e] : s[u][e];
+                  z = seen[u];
+                }
+              wk2[e] = __shfl_sync(FULL, y, src);
+              sk[e] = (__shfl_sync(FULL, z, src) >> (2 * x + e)) & 1u;
+            }
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float val = value_at<D, kF8>(sm.v[st], k0 + kk, d_of(c, y));
+                if (isfinite(val)) continue;
+                if (sk[0]) acc[c][2 * y] = fmaf(wk2[0], val, acc[c][2 * y]);
+                if (sk[1]) acc[c][2 * y + 1] = fmaf(wk2[1], val, acc[c][2 * y + 1]);
+              }
+          }
+        }
+      };
+      if (j0 < all_first || j0 + kTile / 4 > all_last || bad_bits) keys(std::true_type());
+      else keys(std::false_type());
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
     }
-    // every copy lands before this block's shared memory is released
-    if (lane == 0)
-      for (int i = max(0, ring - kStages); i < ring; ++i) mbar_drain(&sm.full[i % kStages], (i / kStages) & 1, p.wait_ns);
+
+    // ---- the warps' results meet in a stage: rows of D + 4 floats ----
+    const int st = ring % kStages;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(FULL, l[e], d);
+    wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+    constexpr int kLd = D + 4;
+    static_assert(2 * 8 * kLd * 4 <= L::kSide, "two warps' O fit one side of a stage");
+    const auto scratch = [&](int w) { return reinterpret_cast<float*>(w & 2 ? sm.v[st] : sm.k[st]) + (w & 1) * 8 * kLd; };
+    {
+      float* buf = scratch(warp);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* at = buf + (2 * q4 + e) * kLd;
+          if (kF8) {
+            *reinterpret_cast<float2*>(at + d_of(c, 0)) = make_float2(acc[c][e], acc[c][2 + e]);
+          } else {
+            at[d_of(c, 0)] = acc[c][e];
+            at[d_of(c, 1)] = acc[c][2 + e];
+          }
+        }
+      if (g == 0) {
+        sm.ml[warp][2 * q4] = make_float2(m[0], l[0]);
+        sm.ml[warp][2 * q4 + 1] = make_float2(m[1], l[1]);
+      }
+    }
+    consumer_sync();
+    const int c0 = wk.first_block(), c1 = wk.last_block();
+    {
+      const int r = threadIdx.x >> 4, x = threadIdx.x & 15;   // 16 threads a row, float4 columns x + 16 y
+      float mm = -INFINITY, ll = 0.f, f[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sm.ml[w][r].x);
+      const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        f[w] = ex2(sm.ml[w][r].x - base);
+        ll = fmaf(sm.ml[w][r].y, f[w], ll);
+      }
+      if (r < rows) {
+        const int i = r / a.group, hh = h * a.group + r - i * a.group;
+        const float sc = c0 != c1 ? 1.f : ll == 0.f ? 0.f : 1.f / ll;
+        char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
+        const size_t part = wk.part() + r;
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y) {
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(scratch(w) + r * kLd + 4 * x + 64 * y);
+            o.x = fmaf(v.x, f[w], o.x);
+            o.y = fmaf(v.y, f[w], o.y);
+            o.z = fmaf(v.z, f[w], o.z);
+            o.w = fmaf(v.w, f[w], o.w);
+          }
+          if (c0 == c1)
+            *reinterpret_cast<uint2*>(dst + (4 * x + 64 * y) * 2) = make_uint2(pack_bf16x2(o.x * sc, o.y * sc), pack_bf16x2(o.z * sc, o.w * sc));
+          else
+            *reinterpret_cast<float4*>(p.part_o + part * D + 4 * x + 64 * y) = o;
+        }
+        if (x == 0) {
+          if (c0 != c1) p.part_ml[part] = make_float2(mm, ll);
+          else if (float* lse = lse_at(a, b, it.s, i, hh)) *lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+        }
+      }
+    }
+    fence_async_shared();                                     // the stage goes back to TMA
+    consumer_sync();
+    if (lane == 0) mbar_arrive(&sm.empty[st]);
+    ++ring;
+    if (c0 != c1 && ends_last(sm, p, c0, c1)) join_parts<D>(p, it, b, h, c0, c1);
+  } while (wk.next(a));
+}
+
+template <int D, bool kF8, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
+  using L = Layout<D, kF8>;
+  constexpr int kStages = L::kStages, kTile = L::kTile;
+  constexpr int kKeyGroups = 4 / MT, kSteps = kTile / 16 / kKeyGroups;     // 16-key steps of a warp in a tile
+  extern __shared__ uint8_t smem_raw[];
+  Smem<D, kF8>& sm = *reinterpret_cast<Smem<D, kF8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  FewWalk<kTile> wk;
+  if (!set_up<D, kF8>(sm, p, wk)) return;
+  if (warp == 4) {
+    produce<D, kF8, (kKeyGroups > 1)>(sm, kmap, vmap, p, wk);
   } else {
     // =============================== consumers ===============================
     const int rt = warp % MT, kg = warp / MT;                 // row tile, key group
     const int g = lane >> 2, q4 = lane & 3;
-    for (;;) {
-      int t_begin, t_end;
-      tiles(&t_begin, &t_end);
-      if (t_begin >= t_end) {
-        if (item0 + it.cost >= u1) break;
-        next_item();
-        continue;
-      }
+    int ring = 0;                                               // stages used so far
+    do {
+      if (wk.t_begin >= wk.t_end) continue;
+      const Item& it = wk.it;
+      const int b = wk.b, h = wk.h, t_begin = wk.t_begin, t_end = wk.t_end;
       const int rows = it.s.n * a.group;
       // my two rows: r0 = 16 rt + g and r0 + 8; queries straight into the A fragments
       const int r0 = rt * 16 + g;
@@ -355,12 +838,11 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
         const int st = ring % kStages;
         wait(sm, &sm.full[st], (ring / kStages) & 1, p);
         const uint32_t kb = smem_u32(sm.k[st]), vb = smem_u32(sm.v[st]);
-        const unsigned long long bad = sm.bad[st];
         // 16 keys from k0 on; edge: some row does not see some of them
         const auto keys16 = [&](auto edge_tag, const int k0) {
           constexpr bool edge = decltype(edge_tag)::value;
           const int j0 = t * kTile + k0;
-          const unsigned bad16 = (unsigned)(bad >> k0) & 0xffffu;
+          const unsigned bad16 = (unsigned)(sm.bad[st][k0 >> 6] >> (k0 & 63)) & 0xffffu;
           // ---- scores of 16 rows x 16 keys ----
           float s[2][4] = {};
           if (kF8) {
@@ -532,7 +1014,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
 #pragma unroll 1
         for (int step = 0; step < kSteps; ++step) {
           const int k0 = (kg * kSteps + step) * 16, j0 = t * kTile + k0;
-          if (j0 < all_first || j0 + 16 > all_last || ((bad >> k0) & 0xffffu)) keys16(std::true_type(), k0);
+          if (j0 < all_first || j0 + 16 > all_last || ((sm.bad[st][k0 >> 6] >> (k0 & 63)) & 0xffffu)) keys16(std::true_type(), k0);
           else keys16(std::false_type(), k0);
         }
         __syncwarp();
@@ -589,9 +1071,9 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
       }
 
       // ---- the rows' results: complete, or a part of an item that other blocks work on too ----
-      const int c0 = (int)(item0 / share), c1 = (int)((item0 + it.n - 1) / share);
+      const int c0 = wk.first_block(), c1 = wk.last_block();
       if (kg == 0) {
-        const int slot = 2 * blockIdx.x + (item0 < u0 ? 0 : 1);
+        const size_t part = wk.part();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = r0 + 8 * e;
@@ -614,7 +1096,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
             float* lse = lse_at(a, b, it.s, i, hh);
             if (lse && q4 == 0) *lse = l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * 0.6931471805599453f;
           } else {
-            float* dst = p.part_o + ((size_t)slot * kMaxFewRows + r) * D;
+            float* dst = p.part_o + (part + r) * D;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
               if constexpr (kF8) {
@@ -625,74 +1107,39 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
                 *reinterpret_cast<float2*>(dst + 8 * c + 2 * q4) = make_float2(acc[c][2 * e], acc[c][2 * e + 1]);
               }
             }
-            if (q4 == 0) p.part_ml[(size_t)slot * kMaxFewRows + r] = make_float2(m[e], l[e]);
+            if (q4 == 0) p.part_ml[part + r] = make_float2(m[e], l[e]);
           }
         }
       }
-      if (c0 != c1) {
-        __threadfence();
-        consumer_sync();
-        if (threadIdx.x == 0) {
-          const bool done = atomicAdd(p.counters + c0, 1) == c1 - c0;
-          if (done) p.counters[c0] = 0;                        // as the next call finds it
-          sm.last = done;
-        }
-        consumer_sync();
-        if (sm.last) {
-          __threadfence();
-          constexpr int kLanes = D / 4;                        // threads a row, four columns each
-          for (int r = threadIdx.x / kLanes; r < rows; r += kConsumers / kLanes) {
-            const int col = (threadIdx.x % kLanes) * 4;
-            float mm = -INFINITY;
-            for (int c = c0; c <= c1; ++c)
-              mm = fmaxf(mm, __ldcg(&p.part_ml[(size_t)(2 * c + (c == c0)) * kMaxFewRows + r]).x);
-            const float base = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const size_t at = (size_t)(2 * c + (c == c0)) * kMaxFewRows + r;
-              const float2 ml = __ldcg(&p.part_ml[at]);
-              const float4 po = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + col));
-              const float f = ex2(ml.x - base);
-              ll = fmaf(ml.y, f, ll);
-              o.x = fmaf(po.x, f, o.x);
-              o.y = fmaf(po.y, f, o.y);
-              o.z = fmaf(po.z, f, o.z);
-              o.w = fmaf(po.w, f, o.w);
-            }
-            const int i = r / a.group, hh = h * a.group + r - i * a.group;
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
-            *reinterpret_cast<uint2*>(dst + col * 2) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            float* lse = lse_at(a, b, it.s, i, hh);
-            if (lse && col == 0) *lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
-          }
-        }
-      }
-      if (item0 + it.cost >= u1) break;
-      next_item();
-    }
+      if (c0 != c1 && ends_last(sm, p, c0, c1)) join_parts<D>(p, it, b, h, c0, c1);
+    } while (wk.next(a));
   }
 }
 
+// MT row tiles of 16; 0: at most 8 rows
 template <int D, bool kF8, int MT>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p, cudaStream_t st) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const size_t smem = sizeof(Smem<D, kF8>) + 1024;
-  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_few<D, kF8, MT>), smem))) return e;
+  const auto kernel = [] {
+    if constexpr (MT == 0) return attn_row8<D, kF8>;
+    else return attn_few<D, kF8, MT>;
+  }();
+  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem))) return e;
   // no more blocks than there can be tiles
-  const long long tiles = (long long)p.a.seqs.batch * p.a.pool.kv_heads * ((p.a.seqs.max_len + kTile - 1) / kTile + 1);
+  constexpr int kTile = Layout<D, kF8>::kTile;
+  const long long tiles = (long long)p.a.seqs.batch * p.a.pool.kv_heads * ((p.a.seqs.max_len + kTile - 1) / kTile + 1 + p.item_cost);
   const int blocks = (int)min((long long)min(2 * sms, kMaxFewBlocks), tiles);
-  attn_few<D, kF8, MT><<<blocks, kThreads, smem, st>>>(km, vm, p);
+  kernel<<<blocks, kThreads, smem, st>>>(km, vm, p);
   return cudaGetLastError();
 }
 
 template <int D, bool kF8>
 cudaError_t launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Params& p, cudaStream_t st) {
   const long long rows = (long long)p.a.seqs.max_new * p.a.group;
+  if (rows <= 8) return launch<D, kF8, 0>(km, vm, p, st);
   if (rows <= 16) return launch<D, kF8, 1>(km, vm, p, st);
   if (rows <= 32) return launch<D, kF8, 2>(km, vm, p, st);
   return launch<D, kF8, 4>(km, vm, p, st);
@@ -704,7 +1151,8 @@ cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned lo
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.pool.num_pages * a.pool.kv_heads * a.pool.page;
   const int esz = a.pool.dtype == PISA_CACHE_E4M3 ? 1 : 2;
-  const uint32_t box = a.pool.page < kTile ? a.pool.page : kTile;
+  const int tile = esz == 1 ? 128 : 64;
+  const uint32_t box = a.pool.page < tile ? a.pool.page : tile;
   if (!encode_rows(&km, a.pool.k, esz, d, rows, box) || !encode_rows(&vm, a.pool.v, esz, d, rows, box))
     return cudaErrorInvalidValue;
   Params p;
@@ -713,10 +1161,8 @@ cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned lo
   p.counters = reinterpret_cast<int*>(w + kCountersAt);
   p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxFewBlocks * kMaxFewRows);
-  p.min_share = 2;
-  // what an item costs besides its tiles (queries, joining, output), in tiles: bf16 tiles take 1.5 us each, e4m3
-  // tiles 0.8; at 64 sequences x 24 heads of up to 4608 tokens e4m3 takes 287 us with 0, 217 with 4, 206 with 6
-  p.item_cost = esz == 1 ? 6 : 1;
+  p.min_share = MIN_SHARE;
+  p.item_cost = ITEM_COST;
   p.wait_ns = wait_ns;
   if (esz == 1) return d == 64 ? launch_rows<64, true>(km, vm, p, st) : launch_rows<128, true>(km, vm, p, st);
   return d == 64 ? launch_rows<64, false>(km, vm, p, st) : launch_rows<128, false>(km, vm, p, st);
