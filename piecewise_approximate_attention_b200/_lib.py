@@ -129,6 +129,22 @@ def _stream(stream) -> Optional[int]:
     return int(s.cuda_stream)
 
 
+_raw_stream = None
+
+
+def stream_handle(stream, device_index: int) -> int:
+    """The CUDA handle of `stream`, or of the device's current stream; without a torch.cuda.Stream
+    object in between (3 us) where torch offers it."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device_index)
+
+
 # ---------------------------------------------------------------------------------------------
 # Thin wrappers with the ABI's names
 # ---------------------------------------------------------------------------------------------
@@ -292,31 +308,23 @@ def pisa_axis_permutation(grid, order: str, extra_tokens: int = 0):
 # ---------------------------------------------------------------------------------------------
 # Paged key/value cache (include/pisa_cache.h)
 # ---------------------------------------------------------------------------------------------
-def rows_of(x, packed: bool) -> PisaRows:
-    """The token tensor x, packed [T, heads, d] or padded [B, heads, L, d], any strides with a contiguous last axis."""
-    if packed:
-        t, h, _ = x.stride()
-        return PisaRows(x.data_ptr(), x.shape[0], 0, t, h)
-    b, h, t, _ = x.stride()
-    return PisaRows(x.data_ptr(), x.shape[2], b, t, h)
-
-
 def pisa_cache_workspace_bytes(cache: PisaCache) -> int:
     return int(lib().pisa_cache_workspace_bytes(ctypes.byref(cache)))
 
 
-def pisa_cache_append(cache: PisaCache, seqs: PisaSequences, k: PisaRows, v: PisaRows, ws, stream=None):
-    _check(lib().pisa_cache_append(cache, seqs, k, v, _ptr(ws), ws.numel(), _stream(stream)), "pisa_cache_append")
+def pisa_cache_append(cache: PisaCache, seqs: PisaSequences, k: PisaRows, v: PisaRows, ws: int, ws_bytes: int, stream: int):
+    """ws and stream as addresses (stream_handle): these calls are short, and made once a layer and token."""
+    _check(lib().pisa_cache_append(cache, seqs, k, v, ws, ws_bytes, stream), "pisa_cache_append")
 
 
-def pisa_cache_read(cache: PisaCache, seqs: PisaSequences, k: PisaRows, v: PisaRows, ws, stream=None):
-    _check(lib().pisa_cache_read(cache, seqs, k, v, _ptr(ws), ws.numel(), _stream(stream)), "pisa_cache_read")
+def pisa_cache_read(cache: PisaCache, seqs: PisaSequences, k: PisaRows, v: PisaRows, ws: int, ws_bytes: int, stream: int):
+    _check(lib().pisa_cache_read(cache, seqs, k, v, ws, ws_bytes, stream), "pisa_cache_read")
 
 
 def pisa_cache_attention(cache: PisaCache, seqs: PisaSequences, heads: int, causal: bool, window: int,
-                         softmax_scale: float, q: PisaRows, o: PisaRows, lse, ws, stream=None):
-    _check(lib().pisa_cache_attention(cache, seqs, heads, causal, window, softmax_scale, q, o, _ptr(lse), _ptr(ws),
-                                      ws.numel(), _stream(stream)), "pisa_cache_attention")
+                         softmax_scale: float, q: PisaRows, o: PisaRows, lse, ws: int, ws_bytes: int, stream: int):
+    _check(lib().pisa_cache_attention(cache, seqs, heads, causal, window, softmax_scale, q, o, _ptr(lse), ws, ws_bytes,
+                                      stream), "pisa_cache_attention")
 
 
 def pisa_read_device_error(ws, stream=None):

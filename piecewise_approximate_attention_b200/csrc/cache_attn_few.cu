@@ -41,12 +41,6 @@ using namespace sm100;
 constexpr int kConsumers = 128;
 constexpr int kThreads = kConsumers + 32;
 constexpr float kLazyLog2 = 8.f;
-#ifndef ITEM_COST
-#define ITEM_COST (esz == 1 ? 3 : 1)
-#endif
-#ifndef MIN_SHARE
-#define MIN_SHARE 2
-#endif
 constexpr unsigned FULL = 0xffffffffu;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
@@ -93,6 +87,8 @@ struct alignas(1024) Smem {
   uint64_t full[L::kStages], empty[L::kStages];
   unsigned long long bad[L::kStages][L::kTile / 64];      // keys of the tile whose page is no page of the pool, or is not there
   long long scan[kThreads / 32], before;
+  float4 join[kConsumers * 2];               // joining the parts of an item: the groups' O, maxima and sums
+  float2 join_ml[16];
   float2 ml[4][16];                          // maximum and sum of the rows that a warp hands over
   int start_b, abort, last;
 };
@@ -328,8 +324,7 @@ __device__ __forceinline__ bool set_up(S& sm, const Params& p, FewWalk<Layout<D,
   return any;
 }
 
-// The block that ends last joins the parts of an item, in the order of the blocks: 16 threads a row of
-// eight, or kLanes16 = false: D / 4 threads a row.  Consumer warps only; true in that block's threads.
+// Whether this block is the last to end of those that share an item.  Consumer warps only.
 template <typename S>
 __device__ __forceinline__ bool ends_last(S& sm, const Params& p, int c0, int c1) {
   __threadfence();
@@ -344,18 +339,24 @@ __device__ __forceinline__ bool ends_last(S& sm, const Params& p, int c0, int c1
   if (last) __threadfence();
   return last;
 }
-template <int D>
-__device__ __forceinline__ void join_parts(const Params& p, const Item& it, int b, int h, int c0, int c1) {
-  constexpr int kLanes = D / 8;                              // threads a row, eight columns each
+// Joins the parts of an item, in the order of the blocks.  A group of D / 8 threads (eight columns each)
+// takes a row, or, when there are fewer rows than groups, every kSub-th part of one.
+template <int D, typename S>
+__device__ __forceinline__ void join_parts(S& sm, const Params& p, const Item& it, int b, int h, int c0, int c1) {
+  constexpr int kLanes = D / 8, kGroups = kConsumers / kLanes;
   const AttnArgs& a = p.a;
-  const int x = threadIdx.x % kLanes, rows = it.s.n * a.group, parts = c1 - c0 + 1;
+  const int x = threadIdx.x % kLanes, grp = threadIdx.x / kLanes, rows = it.s.n * a.group, parts = c1 - c0 + 1;
+  int subs = 1;                                              // groups a row
+  while (subs < 8 && subs * 2 * rows <= kGroups) subs *= 2;
+  const int sub = grp % subs;
   // uniform trips: the shuffles take whole warps
-  for (int r0 = 0; r0 < rows; r0 += kConsumers / kLanes) {
-    const int r = r0 + threadIdx.x / kLanes, rr = min(r, rows - 1);
+  for (int r0 = 0; r0 < rows; r0 += kGroups / subs) {
+    const int r = r0 + grp / subs, rr = min(r, rows - 1);
     float m = -INFINITY, l = 0.f;
     float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int y0 = 0; y0 < parts; y0 += kLanes) {             // lane x: part y0 + x
-      const float2 ml = y0 + x < parts ? __ldcg(&p.part_ml[part_of(c0 + y0 + x, c0) + rr]) : make_float2(-INFINITY, 0.f);
+    for (int y0 = 0; y0 < parts; y0 += kLanes * subs) {      // lane x: part y0 + x * subs + sub
+      const int mine = y0 + x * subs + sub;
+      const float2 ml = mine < parts ? __ldcg(&p.part_ml[part_of(c0 + mine, c0) + rr]) : make_float2(-INFINITY, 0.f);
       float mx = ml.x;
 #pragma unroll
       for (int d = kLanes / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d, kLanes));
@@ -368,21 +369,53 @@ __device__ __forceinline__ void join_parts(const Params& p, const Item& it, int 
       m = m_new;
 #pragma unroll
       for (int e = 0; e < 2; ++e) o[e] = make_float4(o[e].x * f0, o[e].y * f0, o[e].z * f0, o[e].w * f0);
-#pragma unroll 4
-      for (int y = 0; y < min(kLanes, parts - y0); ++y) {
+      const int left = parts - y0, turns = min(kLanes, (left + subs - 1) / subs);
+#pragma unroll 8
+      for (int y = 0; y < turns; ++y) {
+        const int part = y0 + y * subs + sub;
         const float f = __shfl_sync(FULL, fx, y, kLanes);
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + (part_of(c0 + y0 + y, c0) + rr) * D) + 2 * x;
+        if (part < parts) {
+          const float4* src = reinterpret_cast<const float4*>(p.part_o + (part_of(c0 + part, c0) + rr) * D) + 2 * x;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float4 v = __ldcg(src + e);
-          o[e].x = fmaf(v.x, f, o[e].x);
-          o[e].y = fmaf(v.y, f, o[e].y);
-          o[e].z = fmaf(v.z, f, o[e].z);
-          o[e].w = fmaf(v.w, f, o[e].w);
+          for (int e = 0; e < 2; ++e) {
+            const float4 v = __ldcg(src + e);
+            o[e].x = fmaf(v.x, f, o[e].x);
+            o[e].y = fmaf(v.y, f, o[e].y);
+            o[e].z = fmaf(v.z, f, o[e].z);
+            o[e].w = fmaf(v.w, f, o[e].w);
+          }
         }
       }
     }
-    if (r >= rows) continue;
+    if (subs > 1) {                                          // the groups of a row, in their order
+      consumer_sync();
+      float4* at = reinterpret_cast<float4*>(sm.join) + grp * 2 * kLanes + 2 * x;
+      at[0] = o[0];
+      at[1] = o[1];
+      if (x == 0) sm.join_ml[grp] = make_float2(m, l);
+      consumer_sync();
+      if (sub == 0) {
+        float mm = -INFINITY;
+        for (int y = 0; y < subs; ++y) mm = fmaxf(mm, sm.join_ml[grp + y].x);
+        const float base = mm == -INFINITY ? 0.f : mm;
+        m = mm;
+        l = 0.f;
+        o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < subs; ++y) {
+          const float f = ex2(sm.join_ml[grp + y].x - base);
+          l = fmaf(sm.join_ml[grp + y].y, f, l);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 v = at[y * 2 * kLanes + e];
+            o[e].x = fmaf(v.x, f, o[e].x);
+            o[e].y = fmaf(v.y, f, o[e].y);
+            o[e].z = fmaf(v.z, f, o[e].z);
+            o[e].w = fmaf(v.w, f, o[e].w);
+          }
+        }
+      }
+    }
+    if (r >= rows || sub != 0) continue;
     const int i = r / a.group, hh = h * a.group + r - i * a.group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
@@ -745,7 +778,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
     consumer_sync();
     if (lane == 0) mbar_arrive(&sm.empty[st]);
     ++ring;
-    if (c0 != c1 && ends_last(sm, p, c0, c1)) join_parts<D>(p, it, b, h, c0, c1);
+    if (c0 != c1 && ends_last(sm, p, c0, c1)) join_parts<D>(sm, p, it, b, h, c0, c1);
   } while (wk.next(a));
 }
 
@@ -1111,7 +1144,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
           }
         }
       }
-      if (c0 != c1 && ends_last(sm, p, c0, c1)) join_parts<D>(p, it, b, h, c0, c1);
+      if (c0 != c1 && ends_last(sm, p, c0, c1)) join_parts<D>(sm, p, it, b, h, c0, c1);
     } while (wk.next(a));
   }
 }
@@ -1161,8 +1194,12 @@ cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned lo
   p.counters = reinterpret_cast<int*>(w + kCountersAt);
   p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxFewBlocks * kMaxFewRows);
-  p.min_share = MIN_SHARE;
-  p.item_cost = ITEM_COST;
+  // Shares of at least two places, and no item in more than 24 parts or so: past that, joining them costs more than
+  // the shorter shares save (16 heads on 4, 8000 tokens: 13.2 us, 14.3 with 48 parts, 15.6 with 96).
+  p.min_share = max(2, ((a.seqs.max_len + tile - 1) / tile + 23) / 24);
+  // What an item costs besides its tiles (queries, the warps' join, output), in tiles: without it the blocks with
+  // many short sequences end last (64 sequences x 24 heads of up to 4608 tokens, e4m3: 186 us with 1, 155 with 4).
+  p.item_cost = esz == 1 ? 4 : 3;
   p.wait_ns = wait_ns;
   if (esz == 1) return d == 64 ? launch_rows<64, true>(km, vm, p, st) : launch_rows<128, true>(km, vm, p, st);
   return d == 64 ? launch_rows<64, false>(km, vm, p, st) : launch_rows<128, false>(km, vm, p, st);

@@ -56,17 +56,17 @@ struct Walk {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     item_cost = cost_of_item;
     // places of a sequence and head: a warp a sequence, lanes over its pieces
-    const auto seq_cost = [&](int b) -> long long {
-      Seq s;
+    const auto seq_cost = [&](int seq) -> long long {
+      Seq sq;
       long long c = 0;
-      if (b < a.seqs.batch && load_seq(a.seqs, b, a.q.rows, &s))
-        for (int i = lane; i < pieces_of(a, s); i += 32) c += item_of(a, s, i, item_cost).cost;
+      if (seq < a.seqs.batch && load_seq(a.seqs, seq, a.q.rows, &sq))
+        for (int i = lane; i < pieces_of(a, sq); i += 32) c += item_of(a, sq, i, item_cost).cost;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
       return c;
     };
     long long mine = 0;
-    for (int b = warp; b < a.seqs.batch; b += kWarps) mine += seq_cost(b);
+    for (int seq = warp; seq < a.seqs.batch; seq += kWarps) mine += seq_cost(seq);
     if (lane == 0) sc.scan[warp] = mine;
     __syncthreads();
     long long total = 0;

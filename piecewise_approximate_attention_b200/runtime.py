@@ -116,8 +116,8 @@ class Sequences:
     """Which tokens a call on a PagedCache is about; made by PagedCache.sequences, reusable for any
     number of calls (every layer of a step) while its tensors hold what is meant."""
 
-    def __init__(self, c, packed: bool, total: int, tensors):
-        self.c, self.packed, self.total, self.tensors = c, packed, total, tensors
+    def __init__(self, c, packed: bool, batch: int, tensors):
+        self.c, self.packed, self.batch, self.tensors = c, packed, batch, tensors
 
 
 class PagedCache:
@@ -164,6 +164,7 @@ class PagedCache:
         self.k_exp = buffer(k_exp, shape[:3], torch.uint8, "k_exp") if self.fp8 else None
         self.v_exp = buffer(v_exp, shape[:3], torch.uint8, "v_exp") if self.fp8 else None
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self._ws_at, self._ws_bytes = self.ws.data_ptr(), n
         self.c = C.PisaCache(num_pages, kv_heads, page, head_dim, self.DTYPES[dtype], C._ptr(self.k), C._ptr(self.v),
                              C._ptr(self.k_exp), C._ptr(self.v_exp))
 
@@ -186,25 +187,30 @@ class PagedCache:
                             C._ptr(starts), C._ptr(counts))
         return Sequences(c, starts is not None, batch, (page_table, lens, starts, counts))
 
-    def _rows(self, seqs: Sequences, x, heads: int, name: str):
-        if (x.dtype != self.tdtype or x.device != self.device or x.shape[-1] != self.head_dim or x.stride(-1) != 1 or
-                x.shape[1] != heads):
+    def _rows(self, seqs: Sequences, x, heads: int, name: str) -> C.PisaRows:
+        """The token tensor's address and strides, after checking what the library cannot see."""
+        shape, strides = x.shape, x.stride()
+        if len(shape) != (3 if seqs.packed else 4) or (not seqs.packed and shape[0] != seqs.batch):
+            raise ValueError(f"{name} must be [tokens, heads, d] (packed) or [batch, heads, rows, d] (padded)")
+        if (x.dtype != self.tdtype or x.device != self.device or shape[-1] != self.head_dim or strides[-1] != 1 or
+                shape[1] != heads):
             raise ValueError(f"{name} must be a {self.tdtype} tensor on {self.device} with {heads} heads of "
                              f"{self.head_dim} contiguous elements")
-        if x.dim() != (3 if seqs.packed else 4) or (not seqs.packed and x.shape[0] != seqs.total):
-            raise ValueError(f"{name} must be [tokens, heads, d] (packed) or [batch, heads, rows, d] (padded)")
-        return C.rows_of(x, seqs.packed)
+        if seqs.packed:
+            return C.PisaRows(x.data_ptr(), shape[0], 0, strides[0], strides[1])
+        return C.PisaRows(x.data_ptr(), shape[2], strides[0], strides[2], strides[1])
 
     def _call(self, fn, args, stream):
         """On the cache's device, whatever the current one is."""
         import torch
         if self.device.type != "cuda":
             raise ValueError(f"the cache is on {self.device}: the kernels take CUDA tensors only")
-        if self.device.index == torch.cuda.current_device():
-            fn(*args, self.ws, stream)
+        index = self.device.index
+        if index == torch.cuda.current_device():
+            fn(*args, self._ws_at, self._ws_bytes, C.stream_handle(stream, index))
         else:
-            with torch.cuda.device(self.device):
-                fn(*args, self.ws, stream)
+            with torch.cuda.device(index):
+                fn(*args, self._ws_at, self._ws_bytes, C.stream_handle(stream, index))
 
     def append(self, seqs: Sequences, k, v, stream=None):
         """Stores the new tokens' k and v (kv_heads heads) in their pages."""
@@ -221,12 +227,13 @@ class PagedCache:
         """Attention of the new tokens' q (heads heads) over their sequence's cached tokens, into o.
         ``causal``: no later token is seen; ``window`` > 0: only keys less than that far back.  ``lse``
         (fp32, [tokens, heads] packed or [batch, heads, rows] padded) takes the log of the softmax sum."""
-        import torch
         if o is None:                    # rows that belong to no token are zero in a tensor made here
+            import torch
             o = torch.zeros_like(q)
         if o.shape != q.shape:
             raise ValueError("o must have q's shape")
         if lse is not None:
+            import torch
             shape = q.shape[:-1]
             if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous() or lse.device != self.device:
                 raise ValueError(f"lse must be a contiguous float32 tensor {tuple(shape)} on {self.device}")
