@@ -133,6 +133,24 @@ inline size_t partials_bytes(int d) {
   return 2 * (few > chunk ? few : chunk) * (d + 2) * sizeof(float);
 }
 
+// Launches a kernel that may be scheduled while the one before it in the stream still runs
+// (programmatic stream serialization).  Such a kernel begins with sm100.cuh's griddep_wait() in every
+// thread, before it touches global memory, so that a stream's kernels still follow one another.
+template <typename... K, typename... A>
+cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- launchers ----
 cudaError_t launch_append(const Pool& pool, int head_dim, const Seqs& seqs, const Rows& k, const Rows& v, cudaStream_t st);
 cudaError_t launch_read(const Pool& pool, int head_dim, const Seqs& seqs, const Rows& k, const Rows& v, cudaStream_t st);

@@ -139,6 +139,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  griddep_wait();
   if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk<kKeys, 2 * kRows> w;
   if (w.template start<kThreads>(a, sm.walk, p.item_cost, 1 + p.item_cost)) {
@@ -627,6 +628,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
 // one row at a time.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join(const Params p) {
+  griddep_launch_dependents();
   griddep_wait();
   const AttnArgs& a = p.a;
   const int4 item = p.split[blockIdx.x];
@@ -676,19 +678,8 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
   const size_t smem = sizeof(Smem<D, kF8>) + 1024;
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk<D, kF8>), smem))) return e;
   const int blocks = min(sms, kMaxChunkBlocks);
-  attn_chunk<D, kF8><<<blocks, kThreads, smem, st>>>(km, vm, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // scheduled early, it waits for the attention kernel (griddepcontrol.wait)
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, kMaxChunkRows / 64);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join<D>, p);
+  if ((e = launch_after(attn_chunk<D, kF8>, dim3(blocks), kThreads, smem, st, km, vm, p)) != cudaSuccess) return e;
+  return launch_after(attn_join<D>, dim3(blocks, kMaxChunkRows / 64), 256, 0, st, p);
 }
 
 }  // namespace

@@ -319,6 +319,8 @@ __device__ __forceinline__ bool set_up(S& sm, const Params& p, FewWalk<Layout<D,
     sm.abort = 0;
     fence_mbar_init();
   }
+  griddep_launch_dependents();
+  griddep_wait();
   const bool any = w.start(p.a, sm, p.item_cost, p.min_share);
   __syncthreads();
   return any;
@@ -1165,8 +1167,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
   constexpr int kTile = Layout<D, kF8>::kTile;
   const long long tiles = (long long)p.a.seqs.batch * p.a.pool.kv_heads * ((p.a.seqs.max_len + kTile - 1) / kTile + 1 + p.item_cost);
   const int blocks = (int)min((long long)min(2 * sms, kMaxFewBlocks), tiles);
-  kernel<<<blocks, kThreads, smem, st>>>(km, vm, p);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(blocks), kThreads, smem, st, km, vm, p);
 }
 
 template <int D, bool kF8>

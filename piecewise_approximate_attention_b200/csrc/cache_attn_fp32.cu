@@ -61,6 +61,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fp32(const Params p) {
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();
+  griddep_wait();
   Walk<kKeys, kRows> w;
   if (!w.template start<kThreads>(a, sm.walk, 2, 1)) return;
   // products: rows rx + 16 i, keys kx + 16 j, columns 4 (kx) + 64 j
@@ -361,8 +363,7 @@ cudaError_t launch(const Params& p, cudaStream_t st) {
   const size_t smem = sizeof(Smem<D, kRI>);
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_fp32<D, kRI>), smem))) return e;
   const int per_sm = smem <= 113 * 1024 ? 2 : 1;
-  attn_fp32<D, kRI><<<min(per_sm * sms, kMaxFewBlocks), kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_after(attn_fp32<D, kRI>, dim3(min(per_sm * sms, kMaxFewBlocks)), kThreads, smem, st, p);
 }
 
 }  // namespace

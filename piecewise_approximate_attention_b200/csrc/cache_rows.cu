@@ -7,6 +7,7 @@
 // stored, so that enough bytes are in flight.  A block takes consecutive tokens of one head, which
 // are consecutive in a page and (for [B, H, L, d] tensors) in the token tensor.
 #include "cache.cuh"
+#include "sm100.cuh"
 
 namespace pisa {
 namespace cache {
@@ -71,6 +72,8 @@ template <typename T, int D, bool kF8, bool kAppend>
 __global__ void __launch_bounds__(kThreads) move_rows_kernel(Pool pool, Seqs seqs, Rows kr, Rows vr) {
   constexpr int kLanes = D / kPiece<T>;          // threads a row
   constexpr int kTokens = kThreads / kLanes;     // rows a step
+  sm100::griddep_launch_dependents();
+  sm100::griddep_wait();
   const int b = blockIdx.y, head = blockIdx.x % pool.kv_heads;
   const int t0 = blockIdx.x / pool.kv_heads * (kTokens * kRows);
   Seq s;
@@ -162,9 +165,8 @@ cudaError_t launch(const Pool& pool, const Seqs& seqs, const Rows& k, const Rows
   constexpr int kTile = kThreads / (D / kPiece<T>) * kRows;
   const long long chunks = ((long long)seqs.max_new + kTile - 1) / kTile;
   if (chunks * pool.kv_heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  move_rows_kernel<T, D, kF8, kAppend><<<dim3((unsigned)(chunks * pool.kv_heads), seqs.batch), kThreads, 0, st>>>(
-      pool, seqs, k, v);
-  return cudaGetLastError();
+  return launch_after(move_rows_kernel<T, D, kF8, kAppend>, dim3((unsigned)(chunks * pool.kv_heads), seqs.batch), kThreads, 0, st,
+                      pool, seqs, k, v);
 }
 
 template <bool kAppend>
