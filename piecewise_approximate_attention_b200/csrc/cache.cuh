@@ -104,8 +104,17 @@ struct AttnArgs {
   Rows q, o;
   float* lse;
   int heads, group, causal, window;
+  unsigned group_mul;              // floor(2^32 / group) + 1, 0 for group 1
   float scale_log2;                // softmax_scale * log2(e)
 };
+
+// x / group for 0 <= x < 2^31.  The product with group_mul exceeds x * 2^32 / group by x * e / group with
+// 0 < e <= group: exact while x * group < 2^32, else a division.
+__device__ __forceinline__ int token_of(const AttnArgs& a, int x) {
+  if (a.group_mul == 0u) return x;
+  if ((unsigned long long)(unsigned)x * (unsigned)a.group >> 32) return x / a.group;
+  return (int)__umulhi((unsigned)x, a.group_mul);
+}
 
 // Keys that position p of a sequence of `len` tokens sees: [first, last).
 __device__ __forceinline__ void visible(const AttnArgs& a, int len, int p, int* first, int* last) {

@@ -142,14 +142,18 @@ pisa_status pisa_cache_attention(const pisa_cache* cache, const pisa_sequences* 
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return PISA_ERR_INVALID_ARG;
   if ((s = check_seqs(cache, seqs, ws, ws_bytes, &a.seqs, &empty)) != PISA_OK) return s;
   if (empty) return PISA_OK;
-  // one row of queries is at most max_new * group rows of one key/value head: they are numbered in 31 bits
-  if ((long long)seqs->max_new * (heads / cache->kv_heads) >= 0x7fff0000LL) return PISA_ERR_UNSUPPORTED;
+  // the rows of one sequence and key/value head are numbered in 31 bits, and so are its pairs of a tile of rows and
+  // one of keys (at least 16 and 32 of them)
+  const long long head_rows = (long long)seqs->max_new * (heads / cache->kv_heads);
+  if (head_rows >= 0x7fff0000LL || (head_rows / 16 + 1) * ((long long)seqs->max_len / 32 + 16) >= 0x7fff0000LL)
+    return PISA_ERR_UNSUPPORTED;
   if ((s = check_rows(q, cache, a.seqs, heads, false, &a.q)) != PISA_OK) return s;
   if ((s = check_rows(o, cache, a.seqs, heads, true, &a.o)) != PISA_OK) return s;
   if (q->data == o->data || o->rows < q->rows) return PISA_ERR_INVALID_ARG;
   a.lse = lse;
   a.heads = heads;
   a.group = heads / cache->kv_heads;
+  a.group_mul = a.group == 1 ? 0u : (unsigned)((1ull << 32) / (unsigned)a.group + 1);
   a.causal = causal != 0;
   a.window = window;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;

@@ -79,7 +79,7 @@ struct Params {
   int4* split;               // one a block: the item that begins in it and is shared (sequence, head, pair, parts), parts = 0 for none
   float2* part_ml;           // [2 * blocks][256]
   float* part_o;             // [2 * blocks][D / 4][256][4]: a warp's rows next to one another
-  int item_cost;
+  int item_cost;             // what an item costs besides its tiles, in tiles; < 0: items are not cut (cache_walk.cuh)
   unsigned long long wait_ns;
 };
 
@@ -142,7 +142,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
   griddep_wait();
   if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk<kKeys, 2 * kRows> w;
-  if (w.template start<kThreads>(a, sm.walk, p.item_cost, 1 + p.item_cost)) {
+  if (w.template start<kThreads>(a, sm.walk, p.item_cost, p.item_cost < 0 ? 1 : 1 + p.item_cost)) {
     if (warp < 8) {
       // =========================== softmax and output ===========================
       const int slot = warp >> 2, r = threadIdx.x & (kRows - 1);
@@ -155,35 +155,40 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         const bool active = slot * kRows < w.it.rows;
         const int row = slot * kRows + r, grow_ = 256 * w.p + row;          // of the item, of the head's rows
         const bool valid = row < w.it.rows;
-        const int tok = valid ? grow_ / a.group : 0, head = w.h * a.group + (valid ? grow_ - tok * a.group : 0);
+        const int tok = valid ? token_of(a, grow_) : 0, head = w.h * a.group + (valid ? grow_ - tok * a.group : 0);
         float m = -INFINITY, l = 0.f;
         int first = 0, last = w.s.len;
         if (valid) visible(a, w.s.len, w.s.len - w.s.n + tok, &first, &last);
         if (active) {
           // ---- the slot's queries into shared memory: each warp its own 32 rows, D / 8 lanes a row ----
           constexpr int kLanes = D / 8, kPer = 32 / kLanes;    // rows a step
-          uint4 qv[kLanes];
+          const int c = lane % kLanes, q0 = (warp & 3) * 32 + lane / kLanes;
+          const auto q_at = [&](int qr) { return sm.q[slot] + (c >> 3) * S::kHalf + qr * 128 + (((c & 7) ^ (qr & 7)) << 4); };
           {
-            const int gr0 = 256 * w.p + slot * kRows + (warp & 3) * 32 + lane / kLanes;
-            int i = gr0 / a.group, gm = gr0 - i * a.group;     // token and head of the group, stepped
-#pragma unroll
+            const int gr0 = 256 * w.p + slot * kRows + q0;
+            int i = token_of(a, gr0), gm = gr0 - i * a.group;  // token and head of the group, stepped
+#pragma unroll 2
             for (int x = 0; x < kLanes; ++x) {
-              qv[x] = make_uint4(0, 0, 0, 0);
-              if (gr0 + x * kPer < 256 * w.p + w.it.rows)
-                qv[x] = *reinterpret_cast<const uint4*>(a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row +
-                                                        (long long)(w.h * a.group + gm) * a.q.head + (lane % kLanes) * 16);
+              const bool there = gr0 + x * kPer < 256 * w.p + w.it.rows;       // zeros behind the last row
+              const char* src = there ? a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row +
+                                            (long long)(w.h * a.group + gm) * a.q.head + c * 16
+                                      : a.q.data;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(q_at(q0 + x * kPer))), "l"(src),
+                           "r"(there ? 16 : 0) : "memory");
               gm += kPer;
               while (gm >= a.group) {
                 gm -= a.group;
                 ++i;
               }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
           }
-#pragma unroll
-          for (int x4 = 0; x4 < kLanes; ++x4) {
-            const int qr = (warp & 3) * 32 + lane / kLanes + x4 * kPer, c = lane % kLanes;
-            uint4 u = qv[x4];
-            if constexpr (kF8) {
+          if constexpr (kF8) {
+#pragma unroll 2
+            for (int x4 = 0; x4 < kLanes; ++x4) {              // each lane what it has loaded itself
+              const int qr = q0 + x4 * kPer;
+              uint4* at = reinterpret_cast<uint4*>(q_at(qr));
+              const uint4 u = *at;
               const uint32_t x[4] = {u.x, u.y, u.z, u.w};
               uint32_t mx = 0;
 #pragma unroll
@@ -197,10 +202,9 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 y[e] = pack_f16x2(__uint_as_float(x[e] << 16) * sc, __uint_as_float(x[e] & 0xffff0000u) * sc);
-              u = make_uint4(y[0], y[1], y[2], y[3]);
+              *at = make_uint4(y[0], y[1], y[2], y[3]);
               if (c == 0) sm.row_scale[slot * kRows + qr] = a.scale_log2 * pow2(eq);
             }
-            *reinterpret_cast<uint4*>(sm.q[slot] + (c >> 3) * S::kHalf + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = u;
           }
           fence_async_shared();
           __syncwarp();
@@ -334,7 +338,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           for (int rr = 0; rr < 32; ++rr) {
             const int ir = slot * kRows + (warp & 3) * 32 + rr;
             if (ir >= w.it.rows) break;
-            const int gr = 256 * w.p + ir, i = gr / a.group, hh = w.h * a.group + gr - i * a.group;
+            const int gr = 256 * w.p + ir, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
             const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(
                 a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row + (long long)hh * a.q.head);
             for (int c = lane; c < D; c += 32) qs[c] = to_f32(q[c]);
@@ -401,8 +405,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         aux_sync();
         // keys that all of the item's rows see: tiles inside need no care
         int f0, l0, f1, l1;
-        visible(a, w.s.len, w.s.len - w.s.n + 256 * w.p / a.group, &f0, &l0);
-        visible(a, w.s.len, w.s.len - w.s.n + (256 * w.p + w.it.rows - 1) / a.group, &f1, &l1);
+        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, 256 * w.p), &f0, &l0);
+        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, 256 * w.p + w.it.rows - 1), &f1, &l1);
         const int all_first = max(f0, f1), all_last = min(l0, l1);
         int eu[2] = {0, 0};              // E of K and of V
         for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(256) attn_join(const Params p) {
       o[c].w = fmaf(v.w, f, o[c].w);
     }
   }
-  const int gr = 256 * item.z + r, i = gr / a.group, hh = h * a.group + gr - i * a.group;
+  const int gr = 256 * item.z + r, i = token_of(a, gr), hh = h * a.group + gr - i * a.group;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(a.o.data + b * a.o.seq + (long long)(s.row0 + i) * a.o.row + (long long)hh * a.o.head);
 #pragma unroll
@@ -679,6 +683,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk<D, kF8>), smem))) return e;
   const int blocks = min(sms, kMaxChunkBlocks);
   if ((e = launch_after(attn_chunk<D, kF8>, dim3(blocks), kThreads, smem, st, km, vm, p)) != cudaSuccess) return e;
+  if (p.item_cost < 0) return cudaSuccess;      // no item is cut
   return launch_after(attn_join<D>, dim3(blocks, kMaxChunkRows / 64), 256, 0, st, p);
 }
 
@@ -696,7 +701,10 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned 
   p.split = reinterpret_cast<int4*>(w + kSplitAt);
   p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxChunkBlocks * kMaxChunkRows);
-  p.item_cost = 2;
+  // Short items of which each can have a block to itself are not cut: joining costs 3 us, a tile 2.
+  const long long pieces = ((long long)a.seqs.max_new * a.group + 255) / 256;
+  const bool whole = a.seqs.max_len <= 6 * kKeys && pieces * a.pool.kv_heads * a.seqs.batch <= kMaxChunkBlocks;
+  p.item_cost = whole ? -1 : 2;
   p.wait_ns = wait_ns;
   if (esz == 1) return d == 64 ? launch<64, true>(km, vm, p, st) : launch<128, true>(km, vm, p, st);
   return d == 64 ? launch<64, false>(km, vm, p, st) : launch<128, false>(km, vm, p, st);

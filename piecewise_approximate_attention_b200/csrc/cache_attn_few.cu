@@ -30,7 +30,7 @@
 // some rows see it is taken out of the product and added to those rows alone.
 #include <type_traits>
 
-#include "cache.cuh"
+#include "cache_walk.cuh"
 #include "sm100.cuh"
 
 namespace pisa {
@@ -148,11 +148,6 @@ __device__ __forceinline__ float value_at(const uint8_t* tile, int r, int c) {
     return __half2float(__ushort_as_half((unsigned short)h));
   }
   return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(tile + chunk_at<D, false>(r, c >> 3) + 2 * (c & 7)));
-}
-
-// a / b, by 32 bits where they do.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
 // A block's share of the line, and where it is in it; every warp walks its own copy.
@@ -418,7 +413,7 @@ __device__ __forceinline__ void join_parts(S& sm, const Params& p, const Item& i
       }
     }
     if (r >= rows || sub != 0) continue;
-    const int i = r / a.group, hh = h * a.group + r - i * a.group;
+    const int i = token_of(a, r), hh = h * a.group + r - i * a.group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
     *reinterpret_cast<uint4*>(dst + x * 16) = make_uint4(pack_bf16x2(o[0].x * inv, o[0].y * inv), pack_bf16x2(o[0].z * inv, o[0].w * inv),
@@ -465,7 +460,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
     {
       const char* src = nullptr;
       if (g < rows) {
-        const int i = g / a.group, hh = h * a.group + g - i * a.group;
+        const int i = token_of(a, g), hh = h * a.group + g - i * a.group;
         src = a.q.data + b * a.q.seq + (long long)(it.s.row0 + i) * a.q.row + (long long)hh * a.q.head;
       }
       if constexpr (kF8) {
@@ -506,7 +501,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
       rs[e] = __shfl_sync(FULL, rs_g, r * 4);
       first[e] = last[e] = 0;
       if (r < rows) {
-        visible(a, it.s.len, it.s.len - it.s.n + r / a.group, &first[e], &last[e]);
+        visible(a, it.s.len, it.s.len - it.s.n + token_of(a, r), &first[e], &last[e]);
         all_first = max(all_first, first[e]);
         all_last = min(all_last, last[e]);
       }
@@ -750,7 +745,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
         ll = fmaf(sm.ml[w][r].y, f[w], ll);
       }
       if (r < rows) {
-        const int i = r / a.group, hh = h * a.group + r - i * a.group;
+        const int i = token_of(a, r), hh = h * a.group + r - i * a.group;
         const float sc = c0 != c1 ? 1.f : ll == 0.f ? 0.f : 1.f / ll;
         char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
         const size_t part = wk.part() + r;
@@ -819,7 +814,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
         first[e] = last[e] = 0;
         const char* src = nullptr;
         if (r < rows) {
-          const int i = r / a.group, hh = h * a.group + r - i * a.group;
+          const int i = token_of(a, r), hh = h * a.group + r - i * a.group;
           visible(a, it.s.len, it.s.len - it.s.n + i, &first[e], &last[e]);
           src = a.q.data + b * a.q.seq + (long long)(it.s.row0 + i) * a.q.row + (long long)hh * a.q.head;
         }
@@ -1114,7 +1109,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
           const int r = r0 + 8 * e;
           if (r >= rows) continue;
           if (c0 == c1) {
-            const int i = r / a.group, hh = h * a.group + r - i * a.group;
+            const int i = token_of(a, r), hh = h * a.group + r - i * a.group;
             char* dst = a.o.data + b * a.o.seq + (long long)(it.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
             const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
 #pragma unroll
