@@ -3,9 +3,10 @@
 // The new tokens of a sequence times the group of query heads that share a key/value head are the
 // rows of one product with that head's keys.  An item is up to 256 of these rows: two tiles ("slots")
 // of 128 that walk the same tiles of 128 keys together, so a key tile is read from L2 once for 256
-// rows, and one slot's softmax runs while the tensor core works on the other's products.  As in the
-// few-row kernel all items' key tiles form one line that is cut into equal shares, one a block, and
-// items that several blocks share leave partial results (O, maximum, sum) that a second small kernel joins.
+// rows, and one slot's softmax runs while the tensor core works on the other's products.  Where no item
+// has more than 128 rows (kDual), both slots hold the same rows and take the key tiles in turn, and
+// slot 1 hands its result to slot 0 at the end.  The work is shared out as in cache_walk.cuh; items that several
+// blocks share leave partial results (O, maximum, sum) that a second small kernel joins.
 //
 // Block (one an SM, 16 warps):
 //   warps 0-3, 4-7   softmax and output of slot 0 and 1: thread r owns row r (TMEM lane r).  Per tile
@@ -29,6 +30,8 @@
 // holds a value which is not finite in a tile that only some rows see (0 * NaN would reach the rows
 // that do not), is flagged and its rows are computed by the plain routine of cache_row.cuh.  V rows of
 // stale slots and of missing pages are zeroed.
+#include <type_traits>
+
 #include "cache_row.cuh"
 #include "cache_walk.cuh"
 #include "sm100.cuh"
@@ -47,6 +50,7 @@ constexpr uint32_t kColO = 256;
 constexpr int kStages = 2;
 constexpr int kBelow = 15, kAbove = 7;       // exponents that fp16 holds exactly around E
 
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -62,7 +66,7 @@ struct alignas(1024) Smem {
   uint8_t v[kStages][kTile];
   uint8_t raw[kF8 ? 2 : 1][kF8 ? kKeys * D : 16];        // e4m3 codes as loaded, K and V in turn
   uint8_t raw_exp[2][kKeys];
-  float row_scale[kF8 ? 2 * kRows : 1];                  // raw score -> base-2 logit, but for 2^E
+  float row_scale[2 * kRows];                            // raw score -> base-2 logit, but for 2^E; at an item's end slot 1's (maximum, sum)
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], vready[kStages];
   uint64_t rawfull[2], rawempty[2];
   uint64_t qfull[2], sfull[2], pfull[2][2], odone[2][2], drain;
@@ -79,6 +83,7 @@ struct Params {
   int4* split;               // one a block: the item that begins in it and is shared (sequence, head, pair, parts), parts = 0 for none
   float2* part_ml;           // [2 * blocks][256]
   float* part_o;             // [2 * blocks][D / 4][256][4]: a warp's rows next to one another
+  int log_rows;              // rows of an item: 2^7 or 2^8
   int item_cost;             // what an item costs besides its tiles, in tiles; < 0: items are not cut (cache_walk.cuh)
   unsigned long long wait_ns;
 };
@@ -101,7 +106,7 @@ __device__ __forceinline__ uint32_t range_bits(int j0, int first, int last) {
   return m;
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, bool kDual>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
   using S = Smem<D, kF8>;
@@ -141,8 +146,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
   const uint32_t tmem = sm.tmem;
   griddep_wait();
   if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
-  Walk<kKeys, 2 * kRows> w;
-  if (w.template start<kThreads>(a, sm.walk, p.item_cost, p.item_cost < 0 ? 1 : 1 + p.item_cost)) {
+  Walk<kKeys> w;
+  if (w.template start<kThreads>(a, sm.walk, p.log_rows, p.item_cost, p.item_cost < 0 ? 1 : 1 + p.item_cost)) {
     if (warp < 8) {
       // =========================== softmax and output ===========================
       const int slot = warp >> 2, r = threadIdx.x & (kRows - 1);
@@ -152,8 +157,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         if (w.t_begin >= w.t_end) continue;
         const uint32_t tile0 = all_tiles;
         all_tiles += w.t_end - w.t_begin;
-        const bool active = slot * kRows < w.it.rows;
-        const int row = slot * kRows + r, grow_ = 256 * w.p + row;          // of the item, of the head's rows
+        const bool active = kDual || slot * kRows < w.it.rows;
+        const int row = (kDual ? 0 : slot * kRows) + r, grow_ = w.row0() + row;          // of the item, of the head's rows
         const bool valid = row < w.it.rows;
         const int tok = valid ? token_of(a, grow_) : 0, head = w.h * a.group + (valid ? grow_ - tok * a.group : 0);
         float m = -INFINITY, l = 0.f;
@@ -165,11 +170,11 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           const int c = lane % kLanes, q0 = (warp & 3) * 32 + lane / kLanes;
           const auto q_at = [&](int qr) { return sm.q[slot] + (c >> 3) * S::kHalf + qr * 128 + (((c & 7) ^ (qr & 7)) << 4); };
           {
-            const int gr0 = 256 * w.p + slot * kRows + q0;
+            const int gr0 = w.row0() + (kDual ? 0 : slot * kRows) + q0;
             int i = token_of(a, gr0), gm = gr0 - i * a.group;  // token and head of the group, stepped
 #pragma unroll 2
             for (int x = 0; x < kLanes; ++x) {
-              const bool there = gr0 + x * kPer < 256 * w.p + w.it.rows;       // zeros behind the last row
+              const bool there = gr0 + x * kPer < w.row0() + w.it.rows;       // zeros behind the last row
               const char* src = there ? a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row +
                                             (long long)(w.h * a.group + gm) * a.q.head + c * 16
                                       : a.q.data;
@@ -217,12 +222,13 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             all_last = min(all_last, __shfl_xor_sync(FULL, all_last, d));
           }
           float sl = a.scale_log2;       // raw score -> base-2 logit
-          for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
+          const int t_first = w.t_begin + (kDual ? slot : 0);
+          for (int t = t_first; t < w.t_end; t += kDual ? 2 : 1, ++n_tile) {
             const uint32_t par = n_tile & 1;
             wait(sm, &sm.sfull[slot], par, p);
             __syncwarp();
             tc_fence_after();
-            if (kF8 && t == w.t_begin) sl = sm.row_scale[row] * pow2(sm.unit[w.count & 3][0]);
+            if (kF8 && t == t_first) sl = sm.row_scale[slot * kRows + r] * pow2(sm.unit[w.count & 3][0]);
             const uint32_t* bad = sm.bad[(tile0 + t - w.t_begin) & 3];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
@@ -282,7 +288,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
                 f2_unpack(acc2, ls0, ls1);
                 ls = ls0 + ls1;
               };
-              const bool first_half = t == w.t_begin && hh == 0;
+              const bool first_half = t == t_first && hh == 0;
               if (!first_half) weights();
               if (__any_sync(FULL, first_half || ls > kRoom || m == -INFINITY)) {
                 // rare but for the first half: move the maximum, and with it l and O
@@ -322,23 +328,59 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               if (lane == 0) mbar_arrive(&sm.pfull[slot][hh]);
             }
           }
-          wait(sm, &sm.odone[slot][1], (n_tile - 1) & 1, p);
-          __syncwarp();
-          tc_fence_after();
+          if (t_first < w.t_end) {
+            wait(sm, &sm.odone[slot][1], (n_tile - 1) & 1, p);
+            __syncwarp();
+            tc_fence_after();
+          }
         }
+        // ---- dual: slot 1 hands its maximum, sum and O over, through the queries' room ----
+        // (both slots' products have read the queries, and both know of odd values in the last tiles)
+        if (kDual) softmax_sync();
+        const float unit = kF8 ? pow2(sm.unit[w.count & 3][1]) : 1.f;      // O's
+        const bool odd = *reinterpret_cast<volatile int*>(&sm.odd[w.count & 3]) != 0;
+        const bool joined = kDual && w.t_end - w.t_begin > 1 && !odd;                 // slot 1 had tiles, too
+        float4* hand = reinterpret_cast<float4*>(sm.q[0]) + r;                       // [D / 4][128]
+        float2* hand_ml = reinterpret_cast<float2*>(sm.row_scale);
+        float f_own = 1.f, f_other = 0.f;
+        if (joined) {
+          if (slot == 1) {
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              float ov[32];
+              __syncwarp();
+              tmem_ld32(to + 32 * ch, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 8; ++x) hand[(8 * ch + x) * kRows] = make_float4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+            }
+            tc_fence_before();
+            hand_ml[r] = make_float2(m, l);
+          }
+          softmax_sync();
+          if (slot == 0) {
+            const float2 o = hand_ml[r];
+            const float mn = fmaxf(m, o.x), base = mn == -INFINITY ? 0.f : mn;
+            f_own = ex2(m - base);
+            f_other = ex2(o.x - base);
+            m = mn;
+            l = l * f_own + o.y * f_other;
+          }
+        }
+        const bool writes = kDual ? slot == 0 : active;
         // ---- the rows' results: complete, or a part of an item that other blocks work on too ----
         const int c0 = w.first_block(), c1 = w.last_block();
         const size_t part = (size_t)w.part() * 256;
         const auto out_row = [&](int i, int hh) {
           return a.o.data + w.b * a.o.seq + (long long)(w.s.row0 + i) * a.o.row + (long long)hh * a.o.head;
         };
-        if (active && *reinterpret_cast<volatile int*>(&sm.odd[w.count & 3])) {
+        if (writes && odd) {
           // rare: what the operands could not hold, row by row; this warp's rows of the query tile are free as scratch
           float* qs = reinterpret_cast<float*>(sm.q[slot] + (warp & 3) * 32 * 128);
           for (int rr = 0; rr < 32; ++rr) {
-            const int ir = slot * kRows + (warp & 3) * 32 + rr;
+            const int ir = (kDual ? 0 : slot * kRows) + (warp & 3) * 32 + rr;
             if (ir >= w.it.rows) break;
-            const int gr = 256 * w.p + ir, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
+            const int gr = w.row0() + ir, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
             const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(
                 a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row + (long long)hh * a.q.head);
             for (int c = lane; c < D; c += 32) qs[c] = to_f32(q[c]);
@@ -361,8 +403,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               else if (lse) *lse = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
             }
           }
-        } else if (active) {
-          const float unit = kF8 ? pow2(sm.unit[w.count & 3][1]) : 1.f;      // O's
+        } else if (writes) {
           const float inv = (l == 0.f ? 0.f : 1.f / l) * unit;
 #pragma unroll
           for (int ch = 0; ch < D / 32; ++ch) {
@@ -370,6 +411,16 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             __syncwarp();
             tmem_ld32(to + 32 * ch, ov);
             tmem_ld_wait();
+            if (joined) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const float4 o = hand[(8 * ch + x) * kRows];
+                ov[4 * x] = ov[4 * x] * f_own + o.x * f_other;
+                ov[4 * x + 1] = ov[4 * x + 1] * f_own + o.y * f_other;
+                ov[4 * x + 2] = ov[4 * x + 2] * f_own + o.z * f_other;
+                ov[4 * x + 3] = ov[4 * x + 3] * f_own + o.w * f_other;
+              }
+            }
             if (!valid) {
             } else if (c0 == c1) {
               uint4* dst = reinterpret_cast<uint4*>(out_row(tok, head) + 64 * ch);
@@ -390,6 +441,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           }
           tc_fence_before();             // O is read before the next item's first product overwrites it
         }
+        if (kDual) softmax_sync();       // what was handed over has been read: the queries' room is free
         // the block that begins an item which others go on with leaves word of it for the joining kernel
         if (threadIdx.x == 0 && c0 != c1 && !w.began_before()) p.split[blockIdx.x] = make_int4(w.b, w.h, w.p, c1 - c0 + 1);
         ++w.count;
@@ -405,8 +457,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         aux_sync();
         // keys that all of the item's rows see: tiles inside need no care
         int f0, l0, f1, l1;
-        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, 256 * w.p), &f0, &l0);
-        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, 256 * w.p + w.it.rows - 1), &f1, &l1);
+        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0()), &f0, &l0);
+        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0() + w.it.rows - 1), &f1, &l1);
         const int all_first = max(f0, f1), all_last = min(l0, l1);
         int eu[2] = {0, 0};              // E of K and of V
         for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
@@ -503,14 +555,14 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
       }
-      const int box = a.pool.page, boxes = kKeys / box;
+      const int box = a.pool.page, log_box = a.pool.page_log2, boxes = kKeys >> log_box;
       constexpr int kHalves = kF8 ? 1 : D / 64;
       const uint32_t box_bytes = (uint32_t)box * D * (kF8 ? 1 : 2) + (kF8 ? (uint32_t)box : 0u);
+      constexpr int kDeep = kF8 ? 1 : kStages;             // tiles loaded ahead (e4m3: converted into two more)
       uint32_t n_tile = 0;
       do {
         for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
-          const int st = n_tile & 1;
-          const uint32_t ph = (n_tile >> 1) & 1;
+          const int st = n_tile % kDeep;
           int row = -1;                  // lane i < boxes: the box's first row of the pool
           const int pos = t * kKeys + lane * box;
           if (lane < boxes && pos < w.s.len && pos + box > w.it.first) {
@@ -521,17 +573,12 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
 #pragma unroll 1
           for (int side = 0; side < 2; ++side) {
             uint64_t* full = kF8 ? &sm.rawfull[side] : side ? &sm.vfull[st] : &sm.kfull[st];
-            if (kF8) {
-              if (n_tile >= 1) wait(sm, &sm.rawempty[side], (n_tile - 1) & 1, p);
-            } else if (n_tile >= kStages) {
-              wait(sm, side ? &sm.vempty[st] : &sm.kempty[st], ph ^ 1u, p);
-            }
+            uint64_t* empty = kF8 ? &sm.rawempty[side] : side ? &sm.vempty[st] : &sm.kempty[st];
+            if (n_tile >= kDeep) wait(sm, empty, (n_tile / kDeep - 1) & 1, p);
             if (side == 0 && lane < 4) { // the tile's missing keys, before anything of it is released
               uint32_t bits = 0;
-              for (int i = 0; i < 32; i += 16) {
-                const int at = (lane * 32 + i) / box;
-                if (!((have >> at) & 1u)) bits |= 0xffffu << i;
-              }
+              for (int i = 0; i < 32; i += 16)
+                if (!((have >> ((lane * 32 + i) >> log_box)) & 1u)) bits |= 0xffffu << i;
               sm.bad[n_tile & 3][lane] = bits;
             }
             __syncwarp();
@@ -540,8 +587,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             const int i = lane / kHalves, half = lane % kHalves;        // boxes * halves <= 16
             const int rr = __shfl_sync(FULL, row, i);
             if (i < boxes && rr >= 0) {
-              uint8_t* dst = kF8 ? sm.raw[side] + i * box * D
-                                 : (side ? sm.v[st] : sm.k[st]) + half * S::kHalf + i * box * 128;
+              uint8_t* dst = kF8 ? sm.raw[side] + i * box * D : (side ? sm.v[st] : sm.k[st]) + half * S::kHalf + i * box * 128;
               tma_load_3d(dst, side ? &vmap : &kmap, full, half * 64, rr, 0);
               if (kF8) bulk_load(sm.raw_exp[side] + i * box, (side ? a.pool.v_exp : a.pool.k_exp) + rr, box, full);
             }
@@ -550,70 +596,96 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       } while (w.next(a));
       // every copy lands before this block's shared memory is released
       if (lane == 0)
-        for (uint32_t i = n_tile > kStages ? n_tile - kStages : 0; i < n_tile; ++i) {
-          if (kF8) {
-            if (i + 1 == n_tile)
-              for (int side = 0; side < 2; ++side) mbar_drain(&sm.rawfull[side], i & 1, p.wait_ns);
-          } else {
-            mbar_drain(&sm.kfull[i & 1], (i >> 1) & 1, p.wait_ns);
-            mbar_drain(&sm.vfull[i & 1], (i >> 1) & 1, p.wait_ns);
-          }
-        }
+        for (uint32_t i = n_tile > kDeep ? n_tile - kDeep : 0; i < n_tile; ++i)
+          for (int side = 0; side < 2; ++side)
+            mbar_drain(kF8 ? &sm.rawfull[side] : side ? &sm.vfull[i % kDeep] : &sm.kfull[i % kDeep], (i / kDeep) & 1, p.wait_ns);
     } else if (warp == 13 && lane == 0) {
       // =============================== MMA issuer ===============================
       constexpr uint32_t idesc_s = kF8 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_pv = kF8 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
-      uint32_t n_tile = 0, n_slot[2] = {0, 0}, n_item[2] = {0, 0};
-      const auto scores = [&](int slot, int st) {
-        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[slot]), 16, 1024), kd = smem_desc_sw128(smem_u32(sm.k[st]), 16, 1024);
+      uint32_t n_tile = 0, n_slot0 = 0, n_slot1 = 0, n_item0 = 0, n_item1 = 0;       // tiles of the block, tiles and items of each slot
+      uint64_t qd[2], kd[2], vd[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        qd[i] = smem_desc_sw128(smem_u32(sm.q[i]), 16, 1024);
+        kd[i] = smem_desc_sw128(smem_u32(sm.k[i]), 16, 1024);
+        vd[i] = smem_desc_sw128(smem_u32(sm.v[i]), S::kHalf, 1024);
+      }
+      // S of the block's n-th tile (stage n & 1) in a slot; `done`: no other slot needs the tile's keys
+      const auto scores = [&](auto slot_tag, uint32_t n, bool done) {
+        constexpr int slot = decltype(slot_tag)::value;
+        const int st = n & 1;
+        wait(sm, &sm.kfull[st], (n >> 1) & 1, p);
+        tc_fence_after();
+        const uint64_t k = st ? kd[1] : kd[0];
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + 128 * slot, qd + off, kd + off, idesc_s, kk > 0);
+          mma_ss(tmem + 128 * slot, qd[slot] + off, k + off, idesc_s, kk > 0);
         }
         mma_commit(&sm.sfull[slot]);
+        if (done) mma_commit(&sm.kempty[st]);
       };
-      const auto values = [&](int slot, int st, bool fresh) {
-        const uint32_t par = n_slot[slot] & 1;
+      // O += P V of the same tile, half by half
+      const auto values = [&](auto slot_tag, uint32_t n, bool fresh, bool done) {
+        constexpr int slot = decltype(slot_tag)::value;
+        const int st = n & 1;
+        uint32_t& n_slot = slot ? n_slot1 : n_slot0;
+        const uint64_t v = st ? vd[1] : vd[0];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          wait(sm, &sm.pfull[slot][hh], par, p);
+          wait(sm, &sm.pfull[slot][hh], n_slot & 1, p);
           tc_fence_after();
-          const uint64_t vd = smem_desc_sw128(smem_u32(sm.v[st]) + 8192 * hh, S::kHalf, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + kColO + 128 * slot, tmem + 128 * slot + 64 * hh + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), idesc_pv,
+            mma_ts(tmem + kColO + 128 * slot, tmem + 128 * slot + 64 * hh + kk * 8, v + ((8192 * hh + kk * 2048) >> 4), idesc_pv,
                    (!fresh || hh > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&sm.odone[slot][hh]);
         }
-        ++n_slot[slot];
+        ++n_slot;
+        if (done) mma_commit(&sm.vempty[st]);
       };
+      const auto ready = [&](uint32_t n) {
+        wait(sm, &sm.vready[n & 1], (n >> 1) & 1, p);
+        tc_fence_after();
+      };
+      constexpr std::integral_constant<int, 0> s0{};
+      constexpr std::integral_constant<int, 1> s1{};
       do {
         if (w.t_begin >= w.t_end) continue;
-        const int slots = w.it.rows > kRows ? 2 : 1;
-        for (int s = 0; s < slots; ++s) wait(sm, &sm.qfull[s], n_item[s]++ & 1, p);
-        wait(sm, &sm.kfull[n_tile & 1], (n_tile >> 1) & 1, p);
-        tc_fence_after();
-        for (int s = 0; s < slots; ++s) scores(s, n_tile & 1);
-        mma_commit(&sm.kempty[n_tile & 1]);
-        for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
-          const int st = n_tile & 1, nst = st ^ 1;
-          const bool more = t + 1 < w.t_end;
-          wait(sm, &sm.vready[st], (n_tile >> 1) & 1, p);
-          tc_fence_after();
-          for (int s = 0; s < slots; ++s) {
-            values(s, st, t == w.t_begin);
-            if (s + 1 == slots) mma_commit(&sm.vempty[st]);
-            if (more) {
-              if (s == 0) {
-                wait(sm, &sm.kfull[nst], ((n_tile + 1) >> 1) & 1, p);
-                tc_fence_after();
-              }
-              scores(s, nst);
-              if (s + 1 == slots) mma_commit(&sm.kempty[nst]);
+        const int n = w.t_end - w.t_begin;
+        const bool both = kDual || w.it.rows > kRows;
+        wait(sm, &sm.qfull[0], n_item0++ & 1, p);
+        if (both) wait(sm, &sm.qfull[1], n_item1++ & 1, p);
+        if constexpr (kDual) {                     // the slots take the tiles in turn
+          scores(s0, n_tile, true);
+          if (n > 1) scores(s1, n_tile + 1, true);
+#pragma unroll 1
+          for (int i = 0; i < n; i += 2) {
+            ready(n_tile + i);
+            values(s0, n_tile + i, i == 0, true);
+            if (i + 2 < n) scores(s0, n_tile + i + 2, true);
+            if (i + 1 < n) {
+              ready(n_tile + i + 1);
+              values(s1, n_tile + i + 1, i == 0, true);
+              if (i + 3 < n) scores(s1, n_tile + i + 3, true);
+            }
+          }
+        } else {
+          scores(s0, n_tile, !both);
+          if (both) scores(s1, n_tile, true);
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+            ready(n_tile + i);
+            values(s0, n_tile + i, i == 0, !both);
+            if (i + 1 < n) scores(s0, n_tile + i + 1, !both);
+            if (both) {
+              values(s1, n_tile + i, i == 0, true);
+              if (i + 1 < n) scores(s1, n_tile + i + 1, true);
             }
           }
         }
+        n_tile += n;
       } while (w.next(a));
       mma_commit(&sm.drain);
       mbar_drain(&sm.drain, 0, p.wait_ns);
@@ -641,7 +713,8 @@ __global__ void __launch_bounds__(256) attn_join(const Params p) {
   Seq s;
   if (!load_seq(a.seqs, b, a.q.rows, &s)) return;
   const int r = blockIdx.y * 64 + (threadIdx.x >> 5) * 8 + (lane & 7);
-  if (256 * item.z + r >= s.n * a.group) return;
+  const int gr = (item.z << p.log_rows) + r;
+  if (r >> p.log_rows || gr >= s.n * a.group) return;
   const auto slot_of = [&](int x) { return (size_t)(2 * (blockIdx.x + x) + (x == 0)) * kMaxChunkRows; };
   float m = -INFINITY, l = 0.f;
   for (int x = 0; x < parts; ++x) m = fmaxf(m, p.part_ml[slot_of(x) + r].x);
@@ -664,7 +737,7 @@ __global__ void __launch_bounds__(256) attn_join(const Params p) {
       o[c].w = fmaf(v.w, f, o[c].w);
     }
   }
-  const int gr = 256 * item.z + r, i = token_of(a, gr), hh = h * a.group + gr - i * a.group;
+  const int i = token_of(a, gr), hh = h * a.group + gr - i * a.group;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(a.o.data + b * a.o.seq + (long long)(s.row0 + i) * a.o.row + (long long)hh * a.o.head);
 #pragma unroll
@@ -674,15 +747,15 @@ __global__ void __launch_bounds__(256) attn_join(const Params p) {
   if (lse && lane < 8) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, bool kDual>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p, cudaStream_t st) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const size_t smem = sizeof(Smem<D, kF8>) + 1024;
-  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk<D, kF8>), smem))) return e;
+  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_chunk<D, kF8, kDual>), smem))) return e;
   const int blocks = min(sms, kMaxChunkBlocks);
-  if ((e = launch_after(attn_chunk<D, kF8>, dim3(blocks), kThreads, smem, st, km, vm, p)) != cudaSuccess) return e;
+  if ((e = launch_after(attn_chunk<D, kF8, kDual>, dim3(blocks), kThreads, smem, st, km, vm, p)) != cudaSuccess) return e;
   if (p.item_cost < 0) return cudaSuccess;      // no item is cut
   return launch_after(attn_join<D>, dim3(blocks, kMaxChunkRows / 64), 256, 0, st, p);
 }
@@ -702,12 +775,22 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned 
   p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxChunkBlocks * kMaxChunkRows);
   // Short items of which each can have a block to itself are not cut: joining costs 3 us, a tile 2.
-  const long long pieces = ((long long)a.seqs.max_new * a.group + 255) / 256;
-  const bool whole = a.seqs.max_len <= 6 * kKeys && pieces * a.pool.kv_heads * a.seqs.batch <= kMaxChunkBlocks;
+  const long long rows_max = (long long)a.seqs.max_new * a.group, pieces = (rows_max + kRows - 1) / kRows;
+  const bool whole = a.seqs.max_len <= 8 * kKeys && pieces * a.pool.kv_heads * a.seqs.batch <= kMaxChunkBlocks;
+  // e4m3 tiles are not ready fast enough for two slots that each want their own (190 against 185 us at 4 x 16 heads,
+  // 100 rows, 30000 keys; bf16 133 against 149, with head_dim 64 107 against 146)
+  const bool dual = whole || (rows_max <= kRows && esz == 2);
+  p.log_rows = dual ? 7 : 8;
   p.item_cost = whole ? -1 : 2;
   p.wait_ns = wait_ns;
-  if (esz == 1) return d == 64 ? launch<64, true>(km, vm, p, st) : launch<128, true>(km, vm, p, st);
-  return d == 64 ? launch<64, false>(km, vm, p, st) : launch<128, false>(km, vm, p, st);
+  const auto go = [&](auto f8, auto dual) {
+    return d == 64 ? launch<64, decltype(f8)::value, decltype(dual)::value>(km, vm, p, st)
+                   : launch<128, decltype(f8)::value, decltype(dual)::value>(km, vm, p, st);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  if (esz == 1) return dual ? go(yes, yes) : go(yes, no);
+  return dual ? go(no, yes) : go(no, no);
 }
 
 }  // namespace cache

@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fp32(const Params p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();
   griddep_wait();
-  Walk<kKeys, kRows> w;
-  if (!w.template start<kThreads>(a, sm.walk, 2, 1)) return;
+  Walk<kKeys> w;
+  if (!w.template start<kThreads>(a, sm.walk, kRI == 4 ? 6 : 4, 2, 1)) return;
   // products: rows rx + 16 i, keys kx + 16 j, columns 4 (kx) + 64 j
   const int rx = (lane >> 3) + 4 * (warp & 3), kx = (lane & 7) + 8 * (warp >> 2);
   // softmax: four threads a row (kRows * 4 threads)
@@ -112,21 +112,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fp32(const Params p) {
       const int r = e / (D / 4), c = e % (D / 4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
-        const int gr = kRows * w.p + r, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
+        const int gr = w.row0() + r, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
         x = *reinterpret_cast<const float4*>(a.q.data + w.b * a.q.seq + (long long)(w.s.row0 + i) * a.q.row +
                                              (long long)hh * a.q.head + c * 16);
       }
       *reinterpret_cast<float4*>(&sm.q[r][4 * c]) = x;
     }
     int first = 0, last = w.s.len;                          // of my softmax row
-    if (soft && sr < rows) visible(a, w.s.len, w.s.len - w.s.n + token_of(a, kRows * w.p + sr), &first, &last);
+    if (soft && sr < rows) visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0() + sr), &first, &last);
     float m = -INFINITY, l = 0.f;
     // keys that all rows see: tiles inside need no care
     int af, al;
     {
       int f1, l1;
-      visible(a, w.s.len, w.s.len - w.s.n + token_of(a, kRows * w.p), &af, &al);
-      visible(a, w.s.len, w.s.len - w.s.n + token_of(a, kRows * w.p + rows - 1), &f1, &l1);
+      visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0()), &af, &al);
+      visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0() + rows - 1), &f1, &l1);
       af = max(af, f1);
       al = min(al, l1);
     }
@@ -268,19 +268,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fp32(const Params p) {
     const int c0 = w.first_block(), c1 = w.last_block();
     const size_t part = (size_t)w.part() * kMaxFewRows;
     const auto finish = [&](int r, float mr, float lr) {    // once a row
-      const int gr = kRows * w.p + r, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
+      const int gr = w.row0() + r, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
       float* lse = lse_at(a, w.b, w.s, i, hh);
       if (lse) *lse = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
     };
     const auto out_row = [&](int r) {
-      const int gr = kRows * w.p + r, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
+      const int gr = w.row0() + r, i = token_of(a, gr), hh = w.h * a.group + gr - i * a.group;
       return reinterpret_cast<float*>(a.o.data + w.b * a.o.seq + (long long)(w.s.row0 + i) * a.o.row + (long long)hh * a.o.head);
     };
     if (odd) {
       // rare: row by row, a warp a row
       for (int r = warp; r < rows; r += kThreads / 32) {
         int f0, l0;
-        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, kRows * w.p + r), &f0, &l0);
+        visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0() + r), &f0, &l0);
         float mr, lr, acc[D / 32];
         row_attention<float, D>(a, w.b, w.h, sm.q[r], max(f0, w.t_begin * kKeys), min(l0, w.t_end * kKeys), &mr, &lr, acc);
         const float inv = lr == 0.f ? 0.f : 1.f / lr;

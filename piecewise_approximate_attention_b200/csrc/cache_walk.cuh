@@ -1,6 +1,6 @@
 // How attention over the cache is shared out among the blocks of a launch.
 //
-// An item is up to kRows rows of one sequence and key/value head (rows: its new tokens times the group
+// An item is up to 2^log_rows rows of one sequence and key/value head (rows: its new tokens times the group
 // of query heads, token by token), with the keys that any of them sees in tiles of kKeys.  All items
 // form one line, sequence by sequence, head by head; in it an item takes a place for each of its tiles
 // and then item_cost places for what it costs besides them.  The line is cut into equal shares, one a
@@ -25,32 +25,34 @@ struct WalkScratch {                  // in shared memory
 };
 
 // Every role of a block walks its own copy.
-template <int kKeys, int kRows>
+template <int kKeys>
 struct Walk {
   struct Item {
     int t0, n, rows, first;           // its tiles are [t0, t0 + n) of the sequence; first: the first key any row sees
-    int cost;
+    int places, cost;                 // places of its tiles, and with what it costs besides
   };
   int b, h, p, pieces, count;         // sequence, head, piece of its rows (of `pieces`); count: for the caller's use
   Seq s;
   Item it;
   long long item0, u0, u1, share;     // places: the item's first, this block's share, and how long shares are
-  int t_begin, t_end, item_cost;      // this block's tiles of the item: none where its share holds only the last places
+  int t_begin, t_end, item_cost, log_rows;      // this block's tiles of the item: none where its share holds only the last places
 
-  static __device__ __forceinline__ int pieces_of(const AttnArgs& a, const Seq& s) { return (s.n * a.group + kRows - 1) / kRows; }
-  static __device__ __forceinline__ Item item_of(const AttnArgs& a, const Seq& s, int p, int item_cost) {
+  __device__ __forceinline__ int pieces_of(const AttnArgs& a, const Seq& s) const { return (s.n * a.group + (1 << log_rows) - 1) >> log_rows; }
+  __device__ __forceinline__ int row0() const { return p << log_rows; }
+  __device__ __forceinline__ Item item_of(const AttnArgs& a, const Seq& s, int p) const {
     Item it;
-    it.rows = min(kRows, s.n * a.group - kRows * p);
+    it.rows = min(1 << log_rows, s.n * a.group - (p << log_rows));
     int f0, l0, f1, l1;
     const int pos = s.len - s.n;
-    visible(a, s.len, pos + token_of(a, kRows * p), &f0, &l0);
-    visible(a, s.len, pos + token_of(a, kRows * p + it.rows - 1), &f1, &l1);
+    visible(a, s.len, pos + token_of(a, p << log_rows), &f0, &l0);
+    visible(a, s.len, pos + token_of(a, (p << log_rows) + it.rows - 1), &f1, &l1);
     // rows that see nothing (before the cache's first position) leave the range to the others
     const int first = l0 > f0 ? f0 : 0, last = max(l0, l1);
     it.first = first;
     it.t0 = first / kKeys;
     it.n = max(1, (last + kKeys - 1) / kKeys - it.t0);      // rows that see nothing are written too
-    it.cost = item_cost < 0 ? 1 : it.n + item_cost;
+    it.places = item_cost < 0 ? 1 : it.n;
+    it.cost = item_cost < 0 ? 1 : it.places + item_cost;
     return it;
   }
 
@@ -63,15 +65,16 @@ struct Walk {
   // Whole block of kThreads; false if the line ends before this block's share.  cost_of_item < 0: items
   // are not cut, each takes one place (for calls with no more of them than blocks).
   template <int kThreads, typename Scratch>
-  __device__ __forceinline__ bool start(const AttnArgs& a, Scratch& sc, int cost_of_item, int min_share) {
+  __device__ __forceinline__ bool start(const AttnArgs& a, Scratch& sc, int log2_rows, int cost_of_item, int min_share) {
     constexpr int kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     item_cost = cost_of_item;
+    log_rows = log2_rows;
     count = 0;
     // the piece of head h that place u0 falls into, `at` places into the line at the head's first; a warp
     const auto find_piece = [&](const Seq& sq, long long at, int* piece, long long* before) {
       for (int i0 = 0;; i0 += 32) {
-        const int n = i0 + lane < pieces_of(a, sq) ? item_of(a, sq, i0 + lane, item_cost).cost : 0;
+        const int n = i0 + lane < pieces_of(a, sq) ? item_of(a, sq, i0 + lane).cost : 0;
         int upto = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -99,12 +102,12 @@ struct Walk {
           sq.len = __shfl_sync(0xffffffffu, mine.len, i);
           sq.n = __shfl_sync(0xffffffffu, mine.n, i);
           int c = 0;
-          for (int x = lane; x < pieces_of(a, sq); x += 32) c += item_of(a, sq, x, item_cost).cost;
+          for (int x = lane; x < pieces_of(a, sq); x += 32) c += item_of(a, sq, x).cost;
           c = __reduce_add_sync(0xffffffffu, c);
           if (lane == i) cost = c;
         }
       } else {
-        for (int x = 0; x < np; ++x) cost += item_of(a, mine, x, item_cost).cost;
+        for (int x = 0; x < np; ++x) cost += item_of(a, mine, x).cost;
       }
       const long long n = (long long)cost * a.pool.kv_heads;
       long long upto = n;
@@ -132,7 +135,7 @@ struct Walk {
       Seq sq;
       long long c = 0;
       if (seq < a.seqs.batch && load_seq(a.seqs, seq, a.q.rows, &sq))
-        for (int i = lane; i < pieces_of(a, sq); i += 32) c += item_of(a, sq, i, item_cost).cost;
+        for (int i = lane; i < pieces_of(a, sq); i += 32) c += item_of(a, sq, i).cost;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
       return c;
@@ -193,7 +196,7 @@ struct Walk {
   }
 
   __device__ __forceinline__ void enter(const AttnArgs& a) {
-    it = item_of(a, s, p, item_cost);
+    it = item_of(a, s, p);
     if (item_cost < 0) {
       t_begin = it.t0;
       t_end = it.t0 + it.n;
@@ -224,7 +227,7 @@ struct Walk {
   // Blocks that work on the item; a block has at most two items that it shares: the one that began before its
   // share (part 2 * block) and the one that goes on after it (part 2 * block + 1).
   __device__ __forceinline__ int first_block() const { return (int)quotient(item0, share); }
-  __device__ __forceinline__ int last_block() const { return item_cost < 0 ? first_block() : (int)quotient(item0 + it.n - 1, share); }
+  __device__ __forceinline__ int last_block() const { return (int)quotient(item0 + it.places - 1, share); }
   __device__ __forceinline__ bool began_before() const { return item0 < u0; }
   __device__ __forceinline__ int part() const { return 2 * blockIdx.x + (began_before() ? 0 : 1); }
 };
