@@ -511,31 +511,47 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               uint8_t* dst = side ? sm.v[st] : sm.k[st];
               const bool edge = t * kKeys < all_first || (t + 1) * kKeys > all_last;
               bool odd = false;
-#pragma unroll 2
-              for (int c = 0; c < D / 16; ++c) {
-                const int cs = D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
-                const uint4 u = *reinterpret_cast<const uint4*>(sm.raw[side] + r * D + cs * 16);
+              const uint8_t* src = sm.raw[side] + r * D;
+              uint8_t* row = dst + r * 128;
+              const int src_x = D == 128 ? r & 7 : (r >> 1) & 3, dst_x = r & 7;       // the swizzles' part of the row
+              const auto chunk = [&](int c, uint32_t* y) {     // 16 codes, times the row's factor
+                const uint4 u = *reinterpret_cast<const uint4*>(src + ((c ^ src_x) << 4));
                 const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                uint32_t y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   const uint32_t h = e4m3x2_to_f16x2((uint16_t)(x[i >> 1] >> (16 * (i & 1))));
                   const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&h), f2);
                   y[i] = *reinterpret_cast<const uint32_t*>(&z);
                 }
-                if (there && far && (x[0] | x[1] | x[2] | x[3])) odd = true;
-                if (!there) {            // a stale NaN times zero
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) y[i] = 0u;
-                } else if (edge && side) {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if ((y[i] & 0x7c00u) == 0x7c00u || (y[i] & 0x7c000000u) == 0x7c000000u) { odd = true; y[i] = 0u; }
-                }
-                uint8_t* row = dst + (c >> 2) * S::kHalf + r * 128;
+                return (x[0] | x[1] | x[2] | x[3]) != 0u;
+              };
+              const auto store = [&](int c, const uint32_t* y) {
+                uint8_t* at = row + (c >> 2) * S::kHalf;
                 const int ch = (2 * c) & 7;
-                *reinterpret_cast<uint4*>(row + ((ch ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+                *reinterpret_cast<uint4*>(at + ((ch ^ dst_x) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(at + (((ch + 1) ^ dst_x) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+              };
+              if (__all_sync(FULL, there && !far) && !(edge && side)) {
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t y[8];
+                  chunk(c, y);
+                  store(c, y);
+                }
+              } else {
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t y[8];
+                  const bool any = chunk(c, y);
+                  if (there && far && any) odd = true;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const bool inf = (y[i] & 0x7c00u) == 0x7c00u || (y[i] & 0x7c000000u) == 0x7c000000u;
+                    if (there && edge && side && inf) odd = true;
+                    if (!there || (edge && side && inf)) y[i] = 0u;     // a stale NaN times zero
+                  }
+                  store(c, y);
+                }
               }
               if (odd) *reinterpret_cast<volatile int*>(&sm.odd[it4]) = 1;
               fence_async_shared();
