@@ -43,7 +43,7 @@ __device__ __forceinline__ void piece(const uint8_t*, uint4 u, float* x) {
 // maximum m (base 2) and sum l, and lane c adds the values to columns c, c + 32, ... of the row (acc).
 // K: element of the pool (float, bf16, uint8_t for e4m3 codes).
 template <typename K, int D>
-__device__ void row_attention(const AttnArgs& a, int b, int kvh, const float* q, int first, int last, float* m_out,
+__device__ __forceinline__ void row_attention(const AttnArgs& a, int b, int kvh, const float* q, int first, int last, float* m_out,
                               float* l_out, float* acc) {
   constexpr int kPer = 16 / (int)sizeof(K), kCols = D / 32;
   const int lane = threadIdx.x & 31;
