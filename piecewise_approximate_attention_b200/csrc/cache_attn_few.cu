@@ -103,7 +103,8 @@ struct Params {
 };
 
 // An item's keys in tiles: tiles [t0, t0 + n) of the sequence, n = 0 for no new token.  In the line it
-// takes n places for its tiles and then p.item_cost for what it costs besides them; cost = 0 if n = 0.
+// takes n places for its tiles and then p.item_cost for what it costs besides them, or one place where
+// items are not cut (p.item_cost < 0); cost = 0 if n = 0.
 struct Item {
   Seq s;
   int t0, n, first;             // first: the first key that any row sees
@@ -119,7 +120,7 @@ __device__ __forceinline__ Item load_item(const AttnArgs& a, int b, int item_cos
   it.first = first;
   it.t0 = first / kTile;
   it.n = max(1, (it.s.len + kTile - 1) / kTile - it.t0);      // an empty sequence's rows are written too
-  it.cost = it.n + item_cost;
+  it.cost = item_cost < 0 ? 1 : it.n + item_cost;
   return it;
 }
 
@@ -224,6 +225,11 @@ struct FewWalk {
   }
   // the tiles of the item that are this block's: none where its share holds only the item's last places
   __device__ __forceinline__ void enter() {
+    if (item_cost < 0) {              // items are not cut
+      t_begin = it.t0;
+      t_end = it.t0 + it.n;
+      return;
+    }
     t_begin = it.t0 + (int)min((long long)it.n, max(0LL, u0 - item0));
     t_end = it.t0 + (int)min((long long)it.n, u1 - item0);
   }
@@ -239,7 +245,7 @@ struct FewWalk {
   }
   // Blocks that work on the item, and this block's part of it: the end (2 * block) or the beginning (+ 1).
   __device__ __forceinline__ int first_block() const { return (int)quotient(item0, share); }
-  __device__ __forceinline__ int last_block() const { return (int)quotient(item0 + it.n - 1, share); }
+  __device__ __forceinline__ int last_block() const { return item_cost < 0 ? first_block() : (int)quotient(item0 + it.n - 1, share); }
   __device__ __forceinline__ size_t part() const { return (size_t)(2 * blockIdx.x + (item0 < u0 ? 0 : 1)) * kMaxFewRows; }
 };
 __device__ __forceinline__ size_t part_of(int block, int first) { return (size_t)(2 * block + (block == first)) * kMaxFewRows; }
@@ -1160,7 +1166,8 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem))) return e;
   // no more blocks than there can be tiles
   constexpr int kTile = Layout<D, kF8>::kTile;
-  const long long tiles = (long long)p.a.seqs.batch * p.a.pool.kv_heads * ((p.a.seqs.max_len + kTile - 1) / kTile + 1 + p.item_cost);
+  const long long tiles = (long long)p.a.seqs.batch * p.a.pool.kv_heads *
+                          (p.item_cost < 0 ? 1 : (p.a.seqs.max_len + kTile - 1) / kTile + 1 + p.item_cost);
   const int blocks = (int)min((long long)min(2 * sms, kMaxFewBlocks), tiles);
   return launch_after(kernel, dim3(blocks), kThreads, smem, st, km, vm, p);
 }
@@ -1192,10 +1199,14 @@ cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned lo
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxFewBlocks * kMaxFewRows);
   // Shares of at least two places, and no item in more than 24 parts or so: past that, joining them costs more than
   // the shorter shares save (16 heads on 4, 8000 tokens: 13.2 us, 14.3 with 48 parts, 15.6 with 96).
-  p.min_share = max(2, ((a.seqs.max_len + tile - 1) / tile + 23) / 24);
+  const long long tiles = (a.seqs.max_len + tile - 1) / tile, items = (long long)a.seqs.batch * a.pool.kv_heads;
+  // Short items of which each can have a block to itself are not cut: joining parts costs 3 us (200 tokens, 4 heads:
+  // 6.4 us whole, 8.2 cut; 577 tokens: 10.3 and 8.8).
+  const bool whole = tiles <= 6 && items <= 148;
+  p.min_share = whole ? 1 : max(2, ((a.seqs.max_len + tile - 1) / tile + 23) / 24);
   // What an item costs besides its tiles (queries, the warps' join, output), in tiles: without it the blocks with
   // many short sequences end last (64 sequences x 24 heads of up to 4608 tokens, e4m3: 186 us with 1, 155 with 4).
-  p.item_cost = esz == 1 ? 4 : 3;
+  p.item_cost = whole ? -1 : esz == 1 ? 4 : 3;
   p.wait_ns = wait_ns;
   if (esz == 1) return d == 64 ? launch_rows<64, true>(km, vm, p, st) : launch_rows<128, true>(km, vm, p, st);
   return d == 64 ? launch_rows<64, false>(km, vm, p, st) : launch_rows<128, false>(km, vm, p, st);
