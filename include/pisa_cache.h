@@ -74,7 +74,8 @@ typedef struct {
 /* A token tensor: element (b, row, head, c) is data[b * seq_stride + row * row_stride +
  * head * head_stride + c], strides in elements (seq_stride is not used for packed sequences).  Rows
  * are `head_dim` contiguous elements; every used stride is a multiple of 16 bytes.  `rows` is the
- * number of rows there are: of the whole tensor (packed) or of each sequence (padded, >= max_new).
+ * number of rows there are: of the whole tensor (packed; data may be null if there is none) or of each
+ * sequence (padded, >= max_new).
  * [B, H, L, d] is {data, L, H*L*d, d, L*d}; packed [T, H, d] is {data, T, 0, H*d, d}. */
 typedef struct {
   void* data;

@@ -157,7 +157,9 @@ cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, size_t sm
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();      // reported here, not by the next call that asks
+  return e;
 }
 
 // ---- launchers ----

@@ -67,7 +67,8 @@ pisa_status check_seqs(const pisa_cache* c, const pisa_sequences* q, void* ws, s
 
 // written: an output, whose rows must not fall on one another.
 pisa_status check_rows(const pisa_rows* r, const pisa_cache* c, const Seqs& s, int heads, bool written, Rows* out) {
-  if (!r || !r->data || !aligned16(r->data) || r->rows < 0) return PISA_ERR_INVALID_ARG;
+  // packed tensors may be empty (every sequence waits): then there is no address, and nothing to check
+  if (!r || r->rows < 0 || !aligned16(r->data) || (!r->data && (r->rows > 0 || !s.starts))) return PISA_ERR_INVALID_ARG;
   const int esz = c->dtype == PISA_CACHE_FP32 ? 4 : 2;
   const bool packed = s.starts != nullptr;
   if (!packed && r->rows < s.max_new) return PISA_ERR_INVALID_ARG;
@@ -113,6 +114,7 @@ pisa_status move_rows(bool append, const pisa_cache* c, const pisa_sequences* q,
   if (empty) return PISA_OK;
   if ((s = check_rows(k, c, seqs, c->kv_heads, !append, &kr)) != PISA_OK) return s;
   if ((s = check_rows(v, c, seqs, c->kv_heads, !append, &vr)) != PISA_OK) return s;
+  if (!kr.data || !vr.data) return kr.data == vr.data ? PISA_OK : PISA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return cuda_status(append ? launch_append(pool, c->head_dim, seqs, kr, vr, st)
                             : launch_read(pool, c->head_dim, seqs, kr, vr, st));
@@ -149,7 +151,8 @@ pisa_status pisa_cache_attention(const pisa_cache* cache, const pisa_sequences* 
     return PISA_ERR_UNSUPPORTED;
   if ((s = check_rows(q, cache, a.seqs, heads, false, &a.q)) != PISA_OK) return s;
   if ((s = check_rows(o, cache, a.seqs, heads, true, &a.o)) != PISA_OK) return s;
-  if (q->data == o->data || o->rows < q->rows) return PISA_ERR_INVALID_ARG;
+  if ((q->data == o->data && q->data) || o->rows < q->rows) return PISA_ERR_INVALID_ARG;
+  if (!q->data) return PISA_OK;
   a.lse = lse;
   a.heads = heads;
   a.group = heads / cache->kv_heads;

@@ -113,6 +113,20 @@ def test_nothing_to_do_launches_nothing(call):
     assert call(_cache(), _seqs(max_new=0)) == C.PISA_OK
 
 
+@pytest.mark.parametrize("call", CALLS)
+def test_an_empty_packed_tensor_is_nothing_to_do(call):
+    none = _rows(data=None, rows=0)
+    assert call(_cache(), _seqs(starts=P), none, none) == C.PISA_OK
+    assert call(_cache(), _seqs(), none, none) == INV                              # padded rows are there
+    assert call(_cache(), _seqs(starts=P), _rows(data=None, rows=1), none) == INV
+
+
+def test_row_numbers_that_do_not_fit_are_refused():
+    assert _attention(_cache(), _seqs(max_new=1 << 30), heads=4, q=_rows(rows=1 << 30), o=_rows(data=2 * P, rows=1 << 30)) == UNS
+    big = dict(max_new=1 << 22, max_pages=1 << 20, max_len=1 << 26)
+    assert _attention(_cache(), _seqs(**big), q=_rows(rows=1 << 22), o=_rows(data=2 * P, rows=1 << 22)) == UNS
+
+
 def test_binding_checks_its_tensors():
     with pytest.raises(ValueError, match="dtype"):
         PagedCache(4, 2, 2, 16, 64, "fp16", device="cpu")

@@ -313,9 +313,9 @@ def test_values_of_very_different_sizes(new):
     c.check()
 
 
-@pytest.mark.parametrize("dtype", ("bf16", "fp32"))
-@pytest.mark.parametrize("bad", [math.nan, math.inf])
-@pytest.mark.parametrize("new,late", [(1, False), (8, False), (8, True), (100, False), (100, True), (200, True)])
+@pytest.mark.parametrize("dtype,bad", [("bf16", math.nan), ("bf16", math.inf), ("fp32", math.nan), ("fp32", math.inf),
+                                       ("e4m3", math.nan)])      # 8-bit rows hold no infinities
+@pytest.mark.parametrize("new,late", [(1, False), (3, True), (8, False), (8, True), (100, False), (100, True), (200, True)])
 def test_what_a_token_does_not_see_has_no_part(dtype, new, late, bad):
     """Keys and values that are not finite reach exactly the tokens that see them."""
     c = Case(dtype, 4, 2, 128, 16, [300], [new], fill=False)
@@ -337,13 +337,84 @@ def test_what_a_token_does_not_see_has_no_part(dtype, new, late, bad):
         if dirty:
             assert bool(got[:, r].isnan().any()), r
             continue
+        clean = [torch.where(x[0].isfinite(), x[0], 0) for x in (c.k, c.v)]       # what is not finite is not seen here
+        clean = [R.quantise(x)[0] if dtype == "e4m3" else x.double() for x in clean]
         for h in range(4):
-            ref = R.attention(c.q[0][h, r:r + 1].double(), c.k[0][h // 2].double(), c.v[0][h // 2].double(), [pos], True, 250,
+            ref = R.attention(c.q[0][h, r:r + 1].double(), clean[0][h // 2], clean[1][h // 2], [pos], True, 250,
                               float(torch.tensor(c.scale, dtype=torch.float32)))
-            keep = [p for p in range(300) if pos - 250 < p <= pos]
-            ref["vmax"] = c.v[0][h // 2][keep].double().abs().max()
             bo, _ = R.bounds(ref, dtype, 128)
             assert bool(((got[h, r].double() - ref["o"][0]).abs() <= bo[0]).all()), (r, h)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [1, 3, 21, 90])
+def test_many_sequences(dtype, new):
+    """More sequences than a warp has lanes, with lengths from nothing to several tiles, some of them idle."""
+    n = 75
+    lens = [(37 * b * b) % 211 for b in range(n)]
+    fresh = [min(m, new if b % 3 else 0) for b, m in enumerate(lens)]
+    Case(dtype, 4, 2, 64, 16, lens, fresh, "packed" if new % 2 else "padded", seed=new).check(rows=(0, 1, 20, 89))
+
+
+def test_no_rows_at_all():
+    c = Case("bf16", 2, 2, 64, 16, [40, 50], [0, 0], max_new=4)
+    before = c.cache.k.clone()
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    c.cache.append(c.seqs, none, none)
+    c.cache.read(c.seqs, none, none.clone())
+    assert c.cache.attention(c.seqs, none).shape == (0, 2, 64)
+    torch.cuda.synchronize()
+    assert c.cache.device_error() == (C.PISA_OK, 0)
+    assert torch.equal(before.view(torch.int16), c.cache.k.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [1, 20, 150])
+def test_pages_before_a_window_may_be_gone(dtype, new):
+    """A sliding window lets a program free the pages behind it: their table entries are not read."""
+    c = Case(dtype, 4, 2, 128, 16, [700], [new])
+    gone = (700 - new - 64 + 1) // 16          # whole pages before what the first new token sees
+    c.seqs.tensors[0][0, :gone] = -1
+    c.check(window=64)
+
+
+def test_the_same_call_twice_gives_the_same_bits():
+    """Parts of an item are joined in the order of the blocks, whichever ends last."""
+    for dtype in DTYPES:
+        for new in (1, 12, 300):
+            c = Case(dtype, 4, 1, 128, 64, [3000], [new], seed=3)
+            q = c.tokens(c.q, 4).cuda()
+            outs = [c.cache.attention(c.seqs, q, softmax_scale=c.scale) for _ in range(4)]
+            assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_long_contexts_of_few_heads(dtype):
+    """One head's keys over many blocks, against torch in float64 on the device."""
+    n, heads, d = 20011, 3, 64
+    g = torch.Generator(device="cuda").manual_seed(6)
+    t = R.DTYPES[dtype]
+    cache = PagedCache(700, heads, 1, 32, d, dtype)
+    k, v = (torch.randn(n, 1, d, generator=g, device="cuda").to(t) for _ in range(2))
+    table = torch.randperm(700, generator=torch.Generator().manual_seed(2))[None, :626].to(torch.int32).cuda()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    whole = cache.sequences(table, i32(n), n, n, starts=i32(0, n))
+    cache.append(whole, k, v)
+    kk, vv = torch.empty_like(k), torch.empty_like(v)
+    cache.read(whole, kk, vv)
+    for new in (1, 4, 20, 130, 1000):
+        q = torch.randn(new, heads, d, generator=g, device="cuda").to(t)
+        o = cache.attention(cache.sequences(table, i32(n), n, new, starts=i32(0, new)), q, softmax_scale=0.125)
+        s = torch.einsum("qhd,kd->hqk", q.double(), kk[:, 0].double()) * 0.125
+        s.masked_fill_(torch.arange(n, device="cuda")[None] > torch.arange(n - new, n, device="cuda")[:, None], -math.inf)
+        w = torch.softmax(s, -1)
+        ref, size = w @ vv[:, 0].double(), w @ vv[:, 0].double().abs()
+        # the bounds of cache_reference.py: |logit| <= 0.125 * 64 * 25
+        weight = {"bf16": 2.0 ** -8, "fp32": 0.0, "e4m3": 2.0 ** -11}[dtype]
+        rel = weight + 2 * ((d + 4) * 2.0 ** -23 * 200 + 2.0 ** -21) + 2 * n * 2.0 ** -23
+        bound = size * rel * 1.01 + R.HALF_STEP[dtype] * ref.abs() + (n * 2.0 ** -24 * vv.double().abs().max() if dtype == "e4m3" else 0)
+        assert bool(((o.transpose(0, 1).double() - ref).abs() <= bound).all()), new
+    assert cache.device_error() == (C.PISA_OK, 0)
 
 
 def test_bad_lengths_and_pages_are_reported_and_not_followed():
