@@ -347,6 +347,45 @@ def test_what_a_token_does_not_see_has_no_part(dtype, new, late, bad):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [3, 21, 150])
+def test_a_query_that_is_not_finite_harms_its_own_row_only(dtype, new):
+    c = Case(dtype, 4, 2, 128, 32, [310], [new])
+    c.q[0][1, 0, 3], c.q[0][2, new - 1, 5] = math.inf, math.nan
+    got = c.split(c.cache.attention(c.seqs, c.tokens(c.q, 4).cuda(), softmax_scale=c.scale))[0]
+    assert bool(got[1, 0].isnan().all()) and bool(got[2, new - 1].isnan().all())
+    for h in range(4):
+        for r in {0, 1, new // 2, new - 1}:
+            if (h, r) in ((1, 0), (2, new - 1)):
+                continue
+            ref = R.attention(c.q[0][h, r:r + 1].double(), c.kv64[0][0][h // 2], c.kv64[1][0][h // 2], [310 - new + r], True, 0,
+                              float(torch.tensor(c.scale, dtype=torch.float32)))
+            bo, _ = R.bounds(ref, dtype, 128)
+            assert bool(((got[h, r].double() - ref["o"][0]).abs() <= bo[0]).all()), (r, h)
+
+
+@pytest.mark.parametrize("new", [4, 100])
+def test_fp32_numbers_of_any_size(new):
+    """Values near the type's ends, and logits that lean on bits a shorter type does not hold."""
+    c = Case("fp32", 2, 1, 64, 16, [200], [new], fill=False)
+    g = torch.Generator().manual_seed(8)
+    c.v[0] *= torch.exp2(torch.randint(-140, 120, c.v[0].shape, generator=g).float())
+    c.v[0][:, 50, 3], c.v[0][:, 51, 4] = 3.4028e38, -3.4028e38
+    c.k[0] = c.k[0] * 2.0 ** -40
+    c.q[0] = c.q[0] * 2.0 ** 40
+    full = Case.__new__(Case)
+    full.__dict__.update(c.__dict__)
+    full.new, full.max_new = list(c.lens), 200
+    c.cache.append(full.sequences(c.lens), full.tokens(c.k, 1).cuda(), full.tokens(c.v, 1).cuda())
+    got = c.split(c.cache.attention(c.seqs, c.tokens(c.q, 2).cuda(), softmax_scale=c.scale))[0]
+    for h in range(2):
+        for r in {0, new // 2, new - 1}:
+            ref = R.attention(c.q[0][h, r:r + 1].double(), c.k[0][0].double(), c.v[0][0].double(), [200 - new + r], True, 0,
+                              float(torch.tensor(c.scale, dtype=torch.float32)))
+            bo, _ = R.bounds(ref, "fp32", 64)
+            assert bool(((got[h, r].double() - ref["o"][0]).abs() <= bo[0]).all()), (r, h)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("new", [1, 3, 21, 90])
 def test_many_sequences(dtype, new):
     """More sequences than a warp has lanes, with lengths from nothing to several tiles, some of them idle."""
