@@ -140,7 +140,7 @@ pisa_status pisa_cache_attention(const pisa_cache* cache, const pisa_sequences* 
   if (s != PISA_OK) return s;
   if (heads < 1 || heads % cache->kv_heads || window < 0) return PISA_ERR_INVALID_ARG;
   if (heads > 65535) return PISA_ERR_UNSUPPORTED;
-  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return PISA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale * 1.4426950408889634f) || !(softmax_scale > 0.f)) return PISA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return PISA_ERR_INVALID_ARG;
   if ((s = check_seqs(cache, seqs, ws, ws_bytes, &a.seqs, &empty)) != PISA_OK) return s;
   if (empty) return PISA_OK;

@@ -229,7 +229,8 @@ class PagedCache:
         (fp32, [tokens, heads] packed or [batch, heads, rows] padded) takes the log of the softmax sum."""
         if o is None:                    # rows that belong to no token are zero in a tensor made here
             import torch
-            o = torch.zeros_like(q)
+            with torch.cuda.stream(stream):
+                o = torch.zeros_like(q)
         if o.shape != q.shape:
             raise ValueError("o must have q's shape")
         if lse is not None:

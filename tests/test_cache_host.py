@@ -99,7 +99,7 @@ def test_bad_workspaces_are_refused():
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(heads=0), INV), (dict(heads=3), INV), (dict(heads=-2), INV), (dict(heads=1 << 20), UNS), (dict(window=-1), INV),
-    (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV),
+    (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(scale=3e38), INV),
     (dict(lse=P + 2), INV), (dict(o=_rows()), INV), (dict(o=_rows(data=2 * P, rows=8), q=_rows(rows=9)), INV),
 ])
 def test_bad_attention_arguments_are_refused(kw, expect):

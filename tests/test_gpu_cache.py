@@ -669,3 +669,18 @@ def test_calls_on_other_streams():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want)
+
+
+def test_an_output_made_by_the_call_belongs_to_its_stream():
+    """The zeros that the call begins with are written before its results, on whichever stream it runs."""
+    c = Case("bf16", 8, 2, 128, 64, [900, 400], [1, 1])
+    want = c.check()
+    q, st = c.tokens(c.q, 8).cuda(), torch.cuda.Stream()
+    x = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        x = x @ x.clamp(-1, 1)               # the current stream is busy for some milliseconds
+    o = c.cache.attention(c.seqs, q, softmax_scale=c.scale, stream=st)
+    st.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
