@@ -158,7 +158,7 @@ pisa_status pisa_cache_attention(const pisa_cache* cache, const pisa_sequences* 
   a.group = heads / cache->kv_heads;
   a.group_mul = a.group == 1 ? 0u : (unsigned)((1ull << 32) / (unsigned)a.group + 1);
   a.causal = causal != 0;
-  a.window = window;
+  a.window = window >= seqs->max_len ? 0 : window;          // no position is that far back (and none less its window passes 32 bits)
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cache->dtype == PISA_CACHE_FP32) return cuda_status(launch_attention_fp32(a, cache->head_dim, ws, st));

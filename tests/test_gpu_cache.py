@@ -684,3 +684,16 @@ def test_an_output_made_by_the_call_belongs_to_its_stream():
     st.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("causal", [True, False])
+def test_windows_as_long_as_the_type_allows(dtype, causal):
+    """More new tokens than the sequence holds: the first ones stand before position 0."""
+    c = Case(dtype, 4, 2, 64, 16, [40, 7], [60, 9], fill=False, max_new=60)
+    whole = Case.__new__(Case)
+    whole.__dict__.update(c.__dict__)
+    whole.new, whole.max_new = list(c.lens), 40
+    c.cache.append(whole.sequences(c.lens), whole.tokens(c.k, 2).cuda(), whole.tokens(c.v, 2).cuda())
+    c.check(causal=causal, window=2 ** 31 - 1)
+    c.check(causal=causal, window=50)
