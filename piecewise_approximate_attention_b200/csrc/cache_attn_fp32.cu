@@ -6,8 +6,8 @@
 // FMAs on packed pairs (fma.f32x2): the scores' pairs are two neighbouring d, so each sum has two
 // halves, the outputs' pairs two neighbouring columns.  Scores pass through shared memory between the
 // products, where four threads a row keep its maximum and sum.  Bound by what shared memory returns: four
-// cycles for each warp's 16-byte loads.  One token of 4 query heads a group over 577 positions 14.7 us,
-// 32 K positions of 32 heads by 4 sequences 460 us.
+// cycles for each warp's 16-byte loads.  One token, 16 heads on 4 (D = 128): 577 positions 15.5 us,
+// 2000 18.5, 8000 35.5; 40 heads on 8, 4 sequences of up to 32760 positions 459 us.
 //
 // attn_split: 64 rows, 16 a warp, by the matrix pipe (mma.m16n8k16).  Every number is cut into three bf16
 // pieces, h + m + l, which keep 24 bits; of the nine products of pieces the six that weigh 2^-16 and
@@ -65,63 +65,113 @@ __device__ __forceinline__ void cp16(void* dst, const void* src, bool there) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The block that ends last joins the parts of an item, in their order; `top`: room for the rows' maxima.
-template <int D, int kT, typename W, typename Out, typename Finish>
-__device__ __forceinline__ void join(const Params& p, const W& w, int& joins, float* top, int rows, int c0, int c1, Out out_row, Finish finish) {
-  const int tid = threadIdx.x;
+// True in the block that ends last of those that share an item: it joins the parts.
+__device__ __forceinline__ bool ends_last(const Params& p, int& joins, int c0, int c1) {
   __threadfence();
   __syncthreads();
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     const bool done = atomicAdd(p.counters + c0, 1) == c1 - c0;
     if (done) p.counters[c0] = 0;                           // as the next call finds it
     joins = done;
   }
   __syncthreads();
-  if (!joins) return;
+  if (!joins) return false;
   __threadfence();
-  constexpr int kLanes = D / 4, kStep = kT / kLanes, kBatch = kT == kThreads ? 1 : 4;      // rows in flight: 16 or 64 to join
-  const auto maximum = [&](int r) {
+  return true;
+}
+__device__ __forceinline__ size_t part_row(int c, int c0, int r) { return (size_t)(2 * c + (c == c0)) * kMaxFewRows + r; }
+__device__ __forceinline__ void add_scaled(float4& x, float f, float4 y) {
+  x.x = fmaf(y.x, f, x.x);
+  x.y = fmaf(y.y, f, x.y);
+  x.z = fmaf(y.z, f, x.z);
+  x.w = fmaf(y.w, f, x.w);
+}
+__device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
+
+// Few rows can have many parts: each group of D / 4 threads sums every kGroups-th, then the groups' sums are added,
+// in their order (2000 positions, 63 parts: 24 us with the parts one after another).  `sums`: [kGroups][16][D].
+template <int D, int kT, typename Out, typename Finish>
+__device__ __forceinline__ void join_few(const Params& p, float* top, float* total, float* sums, int rows, int c0, int c1,
+                                         Out out_row, Finish finish) {
+  constexpr int kLanes = D / 4, kGroups = kT / kLanes;
+  const int tid = threadIdx.x, lane = tid & 31, g = tid / kLanes, col = (tid % kLanes) * 4;
+  for (int r = tid >> 5; r < rows; r += kT / 32) {          // a warp a row: its maximum and sum
+    float mm = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, __ldcg(&p.part_ml[part_row(c, c0, r)]).x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, d));
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float2 ml = __ldcg(&p.part_ml[part_row(c, c0, r)]);
+      ll = fmaf(ml.y, exp2f(ml.x - base), ll);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(FULL, ll, d);
+    if (lane == 0) {
+      top[r] = base;
+      total[r] = ll;
+      finish(r, mm, ll);
+    }
+  }
+  __syncthreads();
+  for (int r = 0; r < rows; ++r) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0 + g; c <= c1; c += kGroups) {
+      const size_t at = part_row(c, c0, r);
+      add_scaled(x, exp2f(__ldcg(&p.part_ml[at]).x - top[r]), __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + col)));
+    }
+    *reinterpret_cast<float4*>(sums + (g * 16 + r) * D + col) = x;
+  }
+  __syncthreads();
+  for (int r = g; r < rows; r += kGroups) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < kGroups; ++y) add_scaled(x, 1.f, *reinterpret_cast<const float4*>(sums + (y * 16 + r) * D + col));
+    *reinterpret_cast<float4*>(out_row(r) + col) = scaled(x, total[r] == 0.f ? 0.f : 1.f / total[r]);
+  }
+}
+
+// Many rows: four of a thread's in flight.
+template <int D, int kT, typename Out, typename Finish>
+__device__ __forceinline__ void join(const Params& p, float* top, int rows, int c0, int c1, Out out_row, Finish finish) {
+  const int tid = threadIdx.x;
+  if (tid < rows) {
     float mm = -INFINITY;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(&p.part_ml[(size_t)(2 * c + (c == c0)) * kMaxFewRows + r]).x);
-    return mm;
-  };
-  if (kBatch > 1) {
-    if (tid < rows) top[tid] = maximum(tid);
-    __syncthreads();
+    for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(&p.part_ml[part_row(c, c0, tid)]).x);
+    top[tid] = mm;
   }
+  __syncthreads();
+  constexpr int kLanes = D / 4, kStep = kT / kLanes, kBatch = 4;
   const int col = (tid % kLanes) * 4;
   for (int r0 = tid / kLanes; r0 < rows; r0 += kBatch * kStep) {
     float mm[kBatch], base[kBatch], ll[kBatch];
     float4 x[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      mm[i] = kBatch > 1 ? top[min(r0 + i * kStep, rows - 1)] : maximum(r0);
+      mm[i] = top[min(r0 + i * kStep, rows - 1)];
       base[i] = mm[i] == -INFINITY ? 0.f : mm[i];
       ll[i] = 0.f;
       x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-#pragma unroll (kBatch == 1 ? 4 : 2)
+#pragma unroll 2
     for (int c = c0; c <= c1; ++c) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const size_t at = (size_t)(2 * c + (c == c0)) * kMaxFewRows + min(r0 + i * kStep, rows - 1);
+        const size_t at = part_row(c, c0, min(r0 + i * kStep, rows - 1));
         const float2 ml = __ldcg(&p.part_ml[at]);
-        const float4 po = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + col));
         const float f = exp2f(ml.x - base[i]);
         ll[i] = fmaf(ml.y, f, ll[i]);
-        x[i].x = fmaf(po.x, f, x[i].x);
-        x[i].y = fmaf(po.y, f, x[i].y);
-        x[i].z = fmaf(po.z, f, x[i].z);
-        x[i].w = fmaf(po.w, f, x[i].w);
+        add_scaled(x[i], f, __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + col)));
       }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = r0 + i * kStep;
       if (r >= rows) break;
-      const float inv = ll[i] == 0.f ? 0.f : 1.f / ll[i];
-      *reinterpret_cast<float4*>(out_row(r) + col) = make_float4(x[i].x * inv, x[i].y * inv, x[i].z * inv, x[i].w * inv);
+      *reinterpret_cast<float4*>(out_row(r) + col) = scaled(x[i], ll[i] == 0.f ? 0.f : 1.f / ll[i]);
       if (col == 0) finish(r, mm[i], ll[i]);
     }
   }
@@ -373,7 +423,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_few(const Params p) {
         }
       }
     }
-    if (c0 != c1) join<D, kThreads>(p, w, sm.last, sm.m, rows, c0, c1, out_row, finish);
+    if (c0 != c1 && ends_last(p, sm.last, c0, c1)) {
+      static_assert(sizeof(sm.k) + sizeof(sm.v) >= kThreads / (D / 4) * 16 * D * sizeof(float), "the groups' sums");
+      join_few<D, kThreads>(p, sm.m, sm.l, &sm.k[0][0][0], rows, c0, c1, out_row, finish);      // over K and V
+    }
   } while (w.next(a));
 }
 
@@ -689,7 +742,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split(const Params p) {
         }
       }
     }
-    if (c0 != c1) join<D, kT>(p, w, sm.last, sm.m, rows, c0, c1, out_row, finish);
+    if (c0 != c1 && ends_last(p, sm.last, c0, c1)) join<D, kT>(p, sm.m, rows, c0, c1, out_row, finish);
   } while (w.next(a));
 }
 
