@@ -30,6 +30,7 @@
 // holds a value which is not finite in a tile that only some rows see (0 * NaN would reach the rows
 // that do not), is flagged and its rows are computed by the plain routine of cache_row.cuh.  V rows of
 // stale slots and of missing pages are zeroed.
+#include <cfloat>
 #include <type_traits>
 
 #include "cache_row.cuh"
@@ -236,7 +237,12 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             wait(sm, &sm.sfull[slot], par, p);
             __syncwarp();
             tc_fence_after();
-            if (kF8 && t == t_first) sl = sm.row_scale[slot * kRows + r] * pow2(sm.unit[w.count & 3][0]);
+            if (kF8 && t == t_first) {
+              // kept a normal number: -inf of a masked score times 0, or a zero score times inf, would be NaN (scores
+              // that it changes the logits of are zero, or their logits below 2^-80 or past fp32 anyway)
+              sl = sm.row_scale[slot * kRows + r] * pow2(sm.unit[w.count & 3][0]);
+              sl = fminf(fmaxf(sl, FLT_MIN), FLT_MAX);
+            }
             const uint32_t* bad = sm.bad[(tile0 + t - w.t_begin) & 3];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
