@@ -36,7 +36,13 @@ extern "C" {
  * A power of two keeps every stored value a bf16 number (reading back is exact) and lets the
  * attention kernels carry it in the exponents of the softmax weights; the limit of 50 is what their
  * fp32 sums can take.  Rows above 448 * 2^50 saturate, an infinity is stored as the largest code,
- * NaN stays NaN. */
+ * NaN stays NaN.
+ *
+ * Attention and read expect an exponent byte in [PISA_CACHE_EXP_MIN, PISA_CACHE_EXP_MAX] in every slot of the
+ * lengths that they are given, and pisa_cache_append writes no other.  A caller whose lengths may cover slots that were
+ * never appended fills the exponents with PISA_CACHE_EXP_MIN, a row of zeros' (zeroed codes with a byte of 0 are not zeros). */
+#define PISA_CACHE_EXP_MIN 77
+#define PISA_CACHE_EXP_MAX 177
 typedef enum { PISA_CACHE_BF16 = 0, PISA_CACHE_FP32 = 1, PISA_CACHE_E4M3 = 2 } pisa_cache_dtype;
 
 typedef struct {

@@ -19,6 +19,7 @@ PISA_MODE_PISA, PISA_MODE_EXACT_ONLY, PISA_MODE_PER_BLOCK = 0, 1, 2
 PISA_DEVERR_WAIT_TIMEOUT, PISA_DEVERR_BAD_SELECTION = 1, 2
 PISA_DEVERR_BAD_PAGE, PISA_DEVERR_BAD_LENGTH = 3, 4
 PISA_CACHE_BF16, PISA_CACHE_FP32, PISA_CACHE_E4M3 = 0, 1, 2
+PISA_CACHE_EXP_MIN, PISA_CACHE_EXP_MAX = 77, 177
 
 SYMBOLS = ("pisa_abi_version", "pisa_num_blocks", "pisa_stats_bytes", "pisa_stats_carve", "pisa_workspace_bytes",
            "pisa_precompute", "pisa_route", "pisa_attention", "pisa_read_device_error", "pisa_status_string",

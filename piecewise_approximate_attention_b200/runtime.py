@@ -127,7 +127,8 @@ class PagedCache:
 
     ``dtype``: "bf16", "fp32", or "e4m3" (8-bit codes with a power-of-two scale per token and head,
     for bf16 tokens).  The pool tensors ``k``, ``v`` [num_pages, kv_heads, page, head_dim] (uint8 codes
-    for e4m3) and ``k_exp``, ``v_exp`` [num_pages, kv_heads, page] (uint8) are allocated here unless given.
+    for e4m3) and ``k_exp``, ``v_exp`` [num_pages, kv_heads, page] (uint8) are allocated here unless given;
+    a pool made here holds zeros.
     One workspace: calls on one PagedCache must not run at the same time on the device.
     """
 
@@ -153,16 +154,18 @@ class PagedCache:
         shape = (num_pages, kv_heads, page, head_dim)
         pool = torch.uint8 if self.fp8 else self.tdtype
 
-        def buffer(x, shape, dtype, name):
+        def buffer(x, shape, dtype, name, fill=0):
             if x is None:
-                return torch.zeros(shape, dtype=dtype, device=self.device)
+                return torch.full(shape, fill, dtype=dtype, device=self.device)
             if tuple(x.shape) != shape or x.dtype != dtype or x.device != self.device or not x.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}")
             return x
 
         self.k, self.v = buffer(k, shape, pool, "k"), buffer(v, shape, pool, "v")
-        self.k_exp = buffer(k_exp, shape[:3], torch.uint8, "k_exp") if self.fp8 else None
-        self.v_exp = buffer(v_exp, shape[:3], torch.uint8, "v_exp") if self.fp8 else None
+        # 2^-50 is the scale that a row of zeros is stored with; a byte of 0 is no scale of the format
+        scale = C.PISA_CACHE_EXP_MIN
+        self.k_exp = buffer(k_exp, shape[:3], torch.uint8, "k_exp", scale) if self.fp8 else None
+        self.v_exp = buffer(v_exp, shape[:3], torch.uint8, "v_exp", scale) if self.fp8 else None
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
         self._ws_at, self._ws_bytes = self.ws.data_ptr(), n
         self.c = C.PisaCache(num_pages, kv_heads, page, head_dim, self.DTYPES[dtype], C._ptr(self.k), C._ptr(self.v),
