@@ -117,6 +117,9 @@ PISA_API pisa_status pisa_cache_read(const pisa_cache* cache, const pisa_sequenc
  * of sequence b has position p = lens[b] - n_b + i and sees the cached positions j with
  *     0 <= j < lens[b],   j <= p if causal != 0,   j > p - window if window > 0:
  *     o = sum_j w_j v_j / sum_j w_j,   w_j = exp(softmax_scale * q . k_j).
+ * Sums, maxima and logits are fp32.  Where products run on the tensor cores the weights enter the one with V in the
+ * type that it asks of them: fp32 pools in three bf16 parts (24 bits), e4m3 pools as fp16 (11 bits), bf16 pools in two
+ * bf16 parts (16 bits) for at most 16 rows (new tokens times heads / kv_heads) and as bf16 (8 bits) for more.
  * Query head h reads key/value head h / (heads / kv_heads).  Without causal, n_b may exceed lens[b]
  * (queries that are not in the cache).  A token that sees nothing gets o = 0 and lse = -inf; a
  * position that a token does not see has no part in its result, whatever is stored there.

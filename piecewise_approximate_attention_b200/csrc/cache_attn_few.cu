@@ -24,6 +24,13 @@
 // little of it from L2); 64 sequences of up to 4608 tokens, 24 heads, e4m3: 155 us (6.1 TB/s).  30 rows on an
 // e4m3 pool are bound by mma.sync's rate instead (358 us where the stream takes 172).
 //
+// bf16 pools: the type of V asks for bf16 weights.  At most 16 rows, a weight enters as two bf16 numbers, itself and
+// what rounding left over (16 bits), which costs nothing beside the stream (326.4 and 327.0 us above; the error against
+// float64 falls from 2.35e-3, the output's rounding and the weights', to 1.67e-3, the output's alone).  Above, where
+// the second product would cost 23% (30 rows) to 38% (60), weights are bf16, off by 2^-8 at most, and O is scaled by
+// the sum of the weights over the sum of the rounded ones, so that a row which one key dominates is not off by
+// that key's rounding (3% at 60 rows).  Sums are of the weights themselves.
+//
 // e4m3 pools: codes become fp16 exactly (one instruction for two), q becomes fp16 with a power of
 // two per row, also exactly, and a key's scales act on the logits: with x_j = s_j + e_j (e_j the
 // exponent of v_j's scale, in base-2 logits) the weight of code row j is 2^(x_j - M), M the maximum of
@@ -415,6 +422,12 @@ __device__ __forceinline__ void join_parts(S& sm, const Params& p, const Item& i
   }
 }
 
+// Two weights as bf16 numbers, and what their rounding left over.
+__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -590,7 +603,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
             for (int x = 0; x < 4; ++x) acc[c][x] *= f[x & 1];
         }
         const float mb[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-        uint32_t pb[kSub][2];
+        [[maybe_unused]] uint32_t pb[kSub][2], pl[kSub][2];   // pl: bf16 weights' second parts
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -605,7 +618,14 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
                 l[e] += y;
               }
             }
-            pb[u][x] = transpose8x8(kF8 ? pack_f16x2(s[u][2 * x], s[u][2 * x + 1]) : pack_bf16x2(s[u][2 * x], s[u][2 * x + 1]));
+            if constexpr (kF8) {
+              pb[u][x] = transpose8x8(pack_f16x2(s[u][2 * x], s[u][2 * x + 1]));
+            } else {
+              uint32_t hi, lo;
+              split_bf16x2(s[u][2 * x], s[u][2 * x + 1], hi, lo);
+              pb[u][x] = transpose8x8(hi);
+              pl[u][x] = transpose8x8(lo);
+            }
           }
         // ---- O^T += V^T P^T; A fragments hold keys 2 q4, 2 q4 + 1 and +8 ----
         uint32_t keep[kSub][2];
@@ -653,6 +673,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
               ldsm4t(vb + chunk_at<D, false>(k0 + 16 * u + (lane >> 4) * 8 + (lane & 7), 2 * c + ((lane >> 3) & 1)), x);
               const uint32_t A[4] = {clean(x[0], u, 0), clean(x[1], u, 0), clean(x[2], u, 1), clean(x[3], u, 1)};
               mma16816<false>(acc[c], A, pb[u][0], pb[u][1]);
+              mma16816<false>(acc[c], A, pl[u][0], pl[u][1]);
             }
           }
         if (edge && __any_sync(FULL, odd)) {
@@ -777,6 +798,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
   using L = Layout<D, kF8>;
   constexpr int kStages = L::kStages, kTile = L::kTile;
   constexpr int kKeyGroups = 4 / MT, kSteps = kTile / 16 / kKeyGroups;     // 16-key steps of a warp in a tile
+  constexpr bool kTwoParts = !kF8 && MT == 1, kRoundedSum = !kF8 && MT > 1;       // how bf16 weights enter P V
   extern __shared__ uint8_t smem_raw[];
   Smem<D, kF8>& sm = *reinterpret_cast<Smem<D, kF8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const AttnArgs& a = p.a;
@@ -854,7 +876,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
       float acc[D / 8][4];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};      // lr: sum of the rounded weights
 
       for (int t = t_begin; t < t_end; ++t, ++ring) {
         const int st = ring % kStages;
@@ -933,6 +955,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
               f[e] = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
               m[e] = mn;
               l[e] *= f[e];
+              if (kRoundedSum) lr[e] *= f[e];
             }
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
@@ -955,12 +978,16 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
                 l[x >> 1] += w[n][x];
               }
             }
-          uint32_t pa[4];
+          [[maybe_unused]] uint32_t pa[4], pl[4];             // pl: bf16 weights' second parts
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              pa[2 * n + e] = kF8 ? pack_f16x2(w[n][2 * e], w[n][2 * e + 1]) : pack_bf16x2(w[n][2 * e], w[n][2 * e + 1]);
+            for (int e = 0; e < 2; ++e) {
+              const int i = 2 * n + e;
+              if constexpr (kTwoParts) split_bf16x2(w[n][2 * e], w[n][2 * e + 1], pa[i], pl[i]);
+              else pa[i] = kF8 ? pack_f16x2(w[n][2 * e], w[n][2 * e + 1]) : pack_bf16x2(w[n][2 * e], w[n][2 * e + 1]);
+              if (kRoundedSum) lr[e] += __uint_as_float(pa[i] << 16) + __uint_as_float(pa[i] & 0xffff0000u);
+            }
           // ---- O += P V ----
           uint32_t keep[2] = {FULL, FULL};                    // edge: my V rows (keys 2 q4, +1, and +8) that exist
           if (edge) {
@@ -1001,8 +1028,12 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
               }
             } else {
               ldsm4t(vb + chunk_at<D, false>(k0 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * c + (lane >> 4)), x);
-              mma16816<false>(acc[2 * c], pa, clean(x[0], 0), clean(x[1], 1));
-              mma16816<false>(acc[2 * c + 1], pa, clean(x[2], 0), clean(x[3], 1));
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t v0 = clean(x[2 * y], 0), v1 = clean(x[2 * y + 1], 1);
+                mma16816<false>(acc[2 * c + y], pa, v0, v1);
+                if constexpr (kTwoParts) mma16816<false>(acc[2 * c + y], pl, v0, v1);
+              }
             }
           }
           if (edge && __any_sync(FULL, odd)) {
@@ -1047,6 +1078,16 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
       for (int e = 0; e < 2; ++e) {
         l[e] += __shfl_xor_sync(FULL, l[e], 1);
         l[e] += __shfl_xor_sync(FULL, l[e], 2);
+        if (kRoundedSum) {
+          lr[e] += __shfl_xor_sync(FULL, lr[e], 1);
+          lr[e] += __shfl_xor_sync(FULL, lr[e], 2);
+          const float c = lr[e] == 0.f ? 1.f : l[e] / lr[e];
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) {
+            acc[x][2 * e] *= c;
+            acc[x][2 * e + 1] *= c;
+          }
+        }
       }
       if (kKeyGroups > 1) {
         const int st = ring % kStages;

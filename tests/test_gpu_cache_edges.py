@@ -1,5 +1,7 @@
 """The paged cache on data at the edges of what it may hold: zeros, slots that were never written,
 scales far apart (needs a B200).  Tolerances are cache_reference.bounds' unless a test says otherwise."""
+import math
+
 import pytest
 import torch
 
@@ -74,3 +76,50 @@ def test_slots_of_a_new_pool_hold_zeros(dtype, new):
     k, v = (torch.full((n, 2, 128), 7.0, dtype=q.dtype, device="cuda") for _ in range(2))
     cache.read(cache.sequences(table, i32(n), 384, n, starts=i32(0, n)), k, v)
     assert bool((k == 0).all()) and bool((v == 0).all())
+
+
+# ---- the weights' own rounding -----------------------------------------------------------------
+@pytest.mark.parametrize("heads,kv,d,lens,new,window", [
+    (1, 1, 128, [70], [1], 0), (16, 2, 128, [577, 90], [1, 1], 0), (5, 1, 64, [300], [3], 0), (4, 2, 64, [1200, 31], [4, 8], 50),
+    (8, 1, 128, [2500], [2], 0), (3, 3, 128, [260, 5], [16, 5], 0)])
+def test_weights_of_few_rows_keep_sixteen_bits(heads, kv, d, lens, new, window):
+    """bf16 pools, at most 16 rows: the bounds of cache_reference with weights that are off by 2^-16 in two parts
+    (half a step of the second, 2^-8 of what the first left over, itself at most 2^-8) instead of 2^-8."""
+    c = Case("bf16", heads, kv, d, 32, lens, new)
+    q = c.tokens(c.q, heads).cuda()
+    got = c.split(c.cache.attention(c.seqs, q, window=window, softmax_scale=c.scale))
+    for b, (n, m) in enumerate(zip(lens, new)):
+        for h in range(heads):
+            kh = h // (heads // kv)
+            ref = R.attention(c.q[b][h].double(), c.kv64[0][b][kh], c.kv64[1][b][kh], list(range(n - m, n)), True, window,
+                              float(torch.tensor(c.scale, dtype=torch.float32)))
+            rel = 2.0 ** -16 + 2 * ((d + 4) * 2.0 ** -23 * ref["size"] + 2.0 ** -21) + 2 * ref["seen"] * 2.0 ** -23
+            bound = ref["mean_abs"] * rel[:, None] * 1.01 + 2.0 ** -8 * ref["o"].abs() + 1e-37
+            assert bool(((got[b][h].double() - ref["o"]).abs() <= bound).all()), (b, h)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "e4m3"))
+@pytest.mark.parametrize("new", [1, 5, 16, 30, 64, 100, 128, 200, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_row_that_one_late_key_dominates(dtype, new, d):
+    """A key whose logit is 7 + log2(1 + 2^-8) above the largest before it, in base 2: its weight against that maximum
+    is where bf16 rounds farthest.  It holds all but 1/129 of the row, so the row is its value, and must not be off by
+    that rounding: half a step of the result's type, and the weights' 2^-8 on the other key's share of twice the
+    largest |v|."""
+    n, late = 300, 256                       # a tile of every kernel further on, taken by the same warp or slot
+    c = Case(dtype, 1, 1, d, 16, [n], [new], scale=math.log(2.0), fill=False)
+    c.q[0] = torch.ones_like(c.q[0])
+    c.k[0] = torch.full_like(c.k[0], -60.0 / d)
+    c.k[0][0, 0] = 0.0
+    c.k[0][0, late] = 0.0
+    # 7 + 0.005615 from numbers that bf16 and e4m3 rows hold: 7.00390625 + 0.00170898
+    c.k[0][0, late, :7] = 1.0
+    c.k[0][0, late, 7] = 2.0 ** -8
+    c.k[0][0, late, 8] = 2.0 ** -9 if dtype == "e4m3" else 7 * 2.0 ** -12
+    stored(c)
+    got = c.split(c.cache.attention(c.seqs, c.tokens(c.q, 1).cuda(), causal=False, softmax_scale=c.scale))[0][0].double()
+    ref = R.attention(c.q[0][0].double(), c.kv64[0][0][0], c.kv64[1][0][0], list(range(n - new, n)), False, 0,
+                      float(torch.tensor(c.scale, dtype=torch.float32)))["o"]
+    step = torch.exp2(torch.floor(torch.log2(ref.abs())) - 7)
+    bound = step / 2 + 2.0 ** -8 / 129 * 2 * c.kv64[1][0].abs().max() + 2.0 ** -18 * ref.abs()
+    assert bool(((got - ref).abs() <= bound).all()), ((got - ref).abs() / bound).max()
