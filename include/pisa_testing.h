@@ -26,6 +26,11 @@ extern "C" {
  * end on whatever the workspace holds. */
 #define PISA_TESTING_FAULT_SKIP_TILE_LOAD 2
 
+/* The load warps of the cache's attention kernels (bf16 and e4m3 pools) do not load the keys of their block's first
+ * tile, so the bounded wait for them runs out: the block must record PISA_DEVERR_WAIT_TIMEOUT, stop loading, wait for the
+ * copies in flight, free its tensor memory and return. */
+#define PISA_TESTING_FAULT_SKIP_KEYS_LOAD 3
+
 /* Sets the fault injected into subsequent bf16 pisa_attention calls of this process and the
  * bounded-wait limit they use (0 = the default of 2 s).  Process-wide, not thread-safe; pass
  * PISA_TESTING_FAULT_NONE and 0 to restore normal behaviour.  Returns PISA_ERR_INVALID_ARG for an
@@ -37,6 +42,11 @@ PISA_API pisa_status pisa_testing_set_attention_fault(int32_t fault, uint64_t wa
  * pre-computation kernels (0 = the default of 2 s).  Process-wide, not thread-safe.  Returns
  * PISA_ERR_INVALID_ARG for an unknown fault. */
 PISA_API pisa_status pisa_testing_set_precompute_fault(int32_t fault, uint64_t wait_limit_ns);
+
+/* The same for subsequent pisa_cache_attention calls on bf16 and e4m3 pools: PISA_TESTING_FAULT_NONE or
+ * PISA_TESTING_FAULT_SKIP_KEYS_LOAD, and the limit of these kernels' waits (0 = the default of 2 s).  Process-wide, not
+ * thread-safe.  Returns PISA_ERR_INVALID_ARG for an unknown fault. */
+PISA_API pisa_status pisa_testing_set_cache_fault(int32_t fault, uint64_t wait_limit_ns);
 
 #ifdef __cplusplus
 }

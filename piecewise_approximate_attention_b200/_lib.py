@@ -26,7 +26,7 @@ SYMBOLS = ("pisa_abi_version", "pisa_num_blocks", "pisa_stats_bytes", "pisa_stat
            "pisa_precompute_noalloc", "pisa_testing_set_attention_fault", "pisa_perblock_workspace_bytes",
            "pisa_permute_rows", "pisa_axis_permutation", "pisa_precompute_zeroth_order", "pisa_precompute_route",
            "pisa_testing_set_precompute_fault", "pisa_cache_workspace_bytes", "pisa_cache_append", "pisa_cache_read",
-           "pisa_cache_attention")
+           "pisa_cache_attention", "pisa_testing_set_cache_fault")
 
 
 class PisaShape(ctypes.Structure):
@@ -95,6 +95,7 @@ def lib() -> ctypes.CDLL:
             "pisa_precompute_noalloc": (i32, [P(PisaShape), vp, vp, vp, P(PisaStats), vp]),
             "pisa_testing_set_attention_fault": (i32, [i32, ctypes.c_uint64]),
             "pisa_testing_set_precompute_fault": (i32, [i32, ctypes.c_uint64]),
+            "pisa_testing_set_cache_fault": (i32, [i32, ctypes.c_uint64]),
             "pisa_permute_rows": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp]),
             "pisa_cache_workspace_bytes": (sz, [P(PisaCache)]),
             "pisa_cache_append": (i32, [P(PisaCache), P(PisaSequences), P(PisaRows), P(PisaRows), vp, sz, vp]),

@@ -167,10 +167,11 @@ cudaError_t launch_append(const Pool& pool, int head_dim, const Seqs& seqs, cons
 cudaError_t launch_read(const Pool& pool, int head_dim, const Seqs& seqs, const Rows& k, const Rows& v, cudaStream_t st);
 // fp32 pools.
 cudaError_t launch_attention_fp32(const AttnArgs& a, int head_dim, void* ws, cudaStream_t st);
+// wait_ns: the limit of the kernels' waits; fault: test-only fault injection (pisa_testing.h), 0 in normal calls.
 // bf16 and e4m3 pools, at most kMaxFewRows rows (new tokens times query heads of a key/value head).
-cudaError_t launch_attention_few(const AttnArgs& a, int head_dim, void* ws, unsigned long long wait_ns, cudaStream_t st);
+cudaError_t launch_attention_few(const AttnArgs& a, int head_dim, void* ws, unsigned long long wait_ns, int fault, cudaStream_t st);
 // bf16 and e4m3 pools, any number of rows.
-cudaError_t launch_attention_chunk(const AttnArgs& a, int head_dim, void* ws, unsigned long long wait_ns, cudaStream_t st);
+cudaError_t launch_attention_chunk(const AttnArgs& a, int head_dim, void* ws, unsigned long long wait_ns, int fault, cudaStream_t st);
 
 }  // namespace cache
 }  // namespace pisa

@@ -2,10 +2,15 @@
 #include <cmath>
 
 #include "cache.cuh"
+#include "pisa_testing.h"
 
 namespace pisa {
 namespace cache {
 namespace {
+
+// test-only fault injection (pisa_testing.h)
+int g_test_fault = PISA_TESTING_FAULT_NONE;
+unsigned long long g_test_wait_ns = 0;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -162,9 +167,17 @@ pisa_status pisa_cache_attention(const pisa_cache* cache, const pisa_sequences* 
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cache->dtype == PISA_CACHE_FP32) return cuda_status(launch_attention_fp32(a, cache->head_dim, ws, st));
+  const unsigned long long wait_ns = g_test_wait_ns ? g_test_wait_ns : kWaitLimitNs;
   if ((long long)seqs->max_new * a.group <= kMaxFewRows)
-    return cuda_status(launch_attention_few(a, cache->head_dim, ws, kWaitLimitNs, st));
-  return cuda_status(launch_attention_chunk(a, cache->head_dim, ws, kWaitLimitNs, st));
+    return cuda_status(launch_attention_few(a, cache->head_dim, ws, wait_ns, g_test_fault, st));
+  return cuda_status(launch_attention_chunk(a, cache->head_dim, ws, wait_ns, g_test_fault, st));
+}
+
+pisa_status pisa_testing_set_cache_fault(int32_t fault, uint64_t wait_limit_ns) {
+  if (fault != PISA_TESTING_FAULT_NONE && fault != PISA_TESTING_FAULT_SKIP_KEYS_LOAD) return PISA_ERR_INVALID_ARG;
+  g_test_fault = fault;
+  g_test_wait_ns = wait_limit_ns;
+  return PISA_OK;
 }
 
 }  // extern "C"

@@ -39,6 +39,7 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "cache_pipe.cuh"
 #include "cache_row.cuh"
 #include "cache_walk.cuh"
 #include "sm100.cuh"
@@ -59,11 +60,13 @@ constexpr int kStages = 2;
 constexpr int kBelow = 15, kAbove = 7;       // exponents that fp16 holds exactly around E
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ bool softmax_or(bool x) {
+  int y;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+               : "=r"(y) : "r"((int)x) : "memory");
+  return y != 0;
 }
+__device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
 template <int D, bool kF8>
 struct alignas(1024) Smem {
@@ -96,16 +99,12 @@ struct Params {
   int log_rows;              // rows of an item: 2^7 or 2^8
   int item_cost;             // what an item costs besides its tiles, in tiles; < 0: items are not cut (cache_walk.cuh)
   unsigned long long wait_ns;
+  int fault;
 };
 
-// After a timeout every wait returns at once and the block runs to its end on whatever its memory
-// holds (the status word says so), so that no warp is left at a barrier.
 template <typename S>
-__device__ __forceinline__ void wait(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
-  if (!mbar_wait_bounded(bar, parity, &sm.abort, p.wait_ns)) {
-    *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-    set_status(p.a.seqs.status, PISA_DEVERR_WAIT_TIMEOUT);
-  }
+__device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
+  return wait_for(sm, bar, parity, p.wait_ns, p.a.seqs.status);
 }
 
 // Bits of 32 keys from j0 on that lie in [first, last).
@@ -375,10 +374,11 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           }
         }
         // ---- dual: slot 1 hands its maximum, sum and O over, through the queries' room ----
-        // (both slots' products have read the queries, and both know of odd values in the last tiles)
-        if (kDual) softmax_sync();
+        // (both slots' products have read the queries, and what one knows of odd values in its last tiles goes for both:
+        // they have to agree on it whatever happens, barriers depend on it)
+        bool odd = *reinterpret_cast<volatile int*>(&sm.odd[w.count & 3]) != 0;
+        if (kDual) odd = softmax_or(odd);
         const float unit = kF8 ? pow2(sm.unit[w.count & 3][1]) : 1.f;      // O's
-        const bool odd = *reinterpret_cast<volatile int*>(&sm.odd[w.count & 3]) != 0;
         const bool joined = kDual && w.t_end - w.t_begin > 1 && !odd;                 // slot 1 had tiles, too
         float4* hand = reinterpret_cast<float4*>(sm.q[0]) + r;                       // [D / 4][128]
         float2* hand_ml = reinterpret_cast<float2*>(sm.row_scale);
@@ -625,9 +625,10 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       constexpr int kHalves = kF8 ? 1 : D / 64;
       const uint32_t box_bytes = (uint32_t)box * D * (kF8 ? 1 : 2) + (kF8 ? (uint32_t)box : 0u);
       constexpr int kDeep = kF8 ? 1 : kStages;             // tiles loaded ahead (e4m3: converted into two more)
-      uint32_t n_tile = 0;
+      uint32_t n_tile = 0, sides = 0;                      // sides: of tiles loaded so far, K and V in turn
+      bool ok = true;
       do {
-        for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
+        for (int t = w.t_begin; ok && t < w.t_end; ++t, ++n_tile) {
           const int st = n_tile % kDeep;
           int row = -1;                  // lane i < boxes: the box's first row of the pool
           const int pos = t * kKeys + lane * box;
@@ -637,10 +638,13 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           }
           const unsigned have = __ballot_sync(FULL, row >= 0);
 #pragma unroll 1
-          for (int side = 0; side < 2; ++side) {
+          for (int side = 0; side < 2; ++side, ++sides) {
             uint64_t* full = kF8 ? &sm.rawfull[side] : side ? &sm.vfull[st] : &sm.kfull[st];
             uint64_t* empty = kF8 ? &sm.rawempty[side] : side ? &sm.vempty[st] : &sm.kempty[st];
-            if (n_tile >= kDeep) wait(sm, empty, (n_tile / kDeep - 1) & 1, p);
+            // warps that gave up on a copy hand its stage back all the same, after they set the abort word
+            if (n_tile >= kDeep) ok = __all_sync(FULL, wait(sm, empty, (n_tile / kDeep - 1) & 1, p) && !aborted(sm));
+            if (!ok) break;
+            if (p.fault && sides == 0) continue;             // a test's: the keys that never come
             if (side == 0 && lane < 4) { // the tile's missing keys, before anything of it is released
               uint32_t bits = 0;
               for (int i = 0; i < 32; i += 16)
@@ -659,12 +663,13 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             }
           }
         }
-      } while (w.next(a));
+      } while (ok && w.next(a));
       // every copy lands before this block's shared memory is released
       if (lane == 0)
-        for (uint32_t i = n_tile > kDeep ? n_tile - kDeep : 0; i < n_tile; ++i)
-          for (int side = 0; side < 2; ++side)
-            mbar_drain(kF8 ? &sm.rawfull[side] : side ? &sm.vfull[i % kDeep] : &sm.kfull[i % kDeep], (i / kDeep) & 1, p.wait_ns);
+        for (uint32_t x = sides > 2 * kDeep ? sides - 2 * kDeep : 0; x < sides; ++x) {
+          const uint32_t i = x >> 1, side = x & 1;
+          mbar_drain(kF8 ? &sm.rawfull[side] : side ? &sm.vfull[i % kDeep] : &sm.kfull[i % kDeep], (i / kDeep) & 1, p.wait_ns);
+        }
     } else if (warp == 13 && lane == 0) {
       // =============================== MMA issuer ===============================
       constexpr uint32_t idesc_s = kF8 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
@@ -829,7 +834,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
 
 }  // namespace
 
-cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned long long wait_ns, cudaStream_t st) {
+cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned long long wait_ns, int fault, cudaStream_t st) {
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.pool.num_pages * a.pool.kv_heads * a.pool.page;
   const int esz = a.pool.dtype == PISA_CACHE_E4M3 ? 1 : 2;
@@ -851,6 +856,7 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned 
   p.log_rows = dual ? 7 : 8;
   p.item_cost = whole ? -1 : 2;
   p.wait_ns = wait_ns;
+  p.fault = fault;
   const auto go = [&](auto f8, auto dual) {
     return d == 64 ? launch<64, decltype(f8)::value, decltype(dual)::value>(km, vm, p, st)
                    : launch<128, decltype(f8)::value, decltype(dual)::value>(km, vm, p, st);

@@ -42,6 +42,7 @@
 // some rows see it is taken out of the product and added to those rows alone.
 #include <type_traits>
 
+#include "cache_pipe.cuh"
 #include "cache_walk.cuh"
 #include "sm100.cuh"
 
@@ -55,10 +56,6 @@ constexpr int kThreads = kConsumers + 32;
 constexpr float kLazyLog2 = 8.f;
 constexpr unsigned FULL = 0xffffffffu;
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <int D, bool kF8>
@@ -91,7 +88,7 @@ struct Params {
   int* counters;             // one a block, zero between calls
   float2* part_ml;           // [2 * blocks][64]: maximum and sum of a partial result's rows
   float* part_o;             // [2 * blocks][64][D]
-  int min_share, item_cost;
+  int min_share, item_cost, fault;
   unsigned long long wait_ns;
 };
 
@@ -117,14 +114,9 @@ __device__ __forceinline__ Item load_item(const AttnArgs& a, int b, int item_cos
   return it;
 }
 
-// Waits for a phase; after a timeout every wait returns at once and the block runs to its end on
-// whatever shared memory holds (the status word says so), so that no warp is left at a barrier.
 template <typename S>
-__device__ __forceinline__ void wait(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
-  if (!mbar_wait_bounded(bar, parity, &sm.abort, p.wait_ns)) {
-    *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-    set_status(p.a.seqs.status, PISA_DEVERR_WAIT_TIMEOUT);
-  }
+__device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
+  return wait_for(sm, bar, parity, p.wait_ns, p.a.seqs.status);
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile as TMA wrote it.
@@ -259,9 +251,10 @@ __device__ __forceinline__ void produce(S& sm, const CUtensorMap& kmap, const CU
   const int box = min(a.pool.page, kTile), log_box = min(a.pool.page_log2, kF8 ? 7 : 6), pages = kTile >> log_box;   // boxes of a tile
   constexpr int per = 2 * L::kHalves;                                  // copies of a box
   const uint32_t box_bytes = 2u * box * D * (kF8 ? 1 : 2) + (kF8 ? 2u * box : 0u);
-  int ring = 0;                                                        // stages used so far
+  int skip = p.fault != 0, ring = skip;                                // stages used so far; skip: a test's stage that never fills
+  bool ok = true;
   do {
-    for (int t = w.t_begin; t < w.t_end; ++t, ++ring) {
+    for (int t = w.t_begin + skip; t < w.t_end; ++t, ++ring) {
       const int st = ring % kStages;
       // lane i < pages looks box i's page up
       int row = -1;
@@ -270,8 +263,11 @@ __device__ __forceinline__ void produce(S& sm, const CUtensorMap& kmap, const CU
         const int pg = load_page(a.seqs, a.pool, w.b, pos);
         if (pg >= 0) row = (pg * a.pool.kv_heads + w.h) * a.pool.page + (pos & (a.pool.page - 1));
       }
-      if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
-      const unsigned have = __ballot_sync(FULL, row >= 0);
+      if (ring >= kStages) ok = wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
+      // one vote for the pages (at most 8) and whether there is room, for all lanes what the last one saw
+      const unsigned have = __ballot_sync(FULL, lane < 31 ? row >= 0 : !ok);
+      ok = !(have >> 31);
+      if (!ok) break;
       if (lane < kTile / 64) {
         unsigned long long bits = 0;
         for (int i = 0; i < 64; i += 16)
@@ -290,13 +286,14 @@ __device__ __forceinline__ void produce(S& sm, const CUtensorMap& kmap, const CU
         if (kF8) bulk_load((side ? sm.ve[st] : sm.ke[st]) + i * box, (side ? a.pool.v_exp : a.pool.k_exp) + r, box, &sm.full[st]);
       }
     }
-    if (kJoin && w.t_begin < w.t_end) {
+    skip = 0;
+    if (kJoin && ok && w.t_begin < w.t_end) {
       const int st = ring % kStages;
-      if (ring >= kStages) wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
-      if (lane == 0) mbar_arrive(&sm.full[st]);
-      ++ring;
+      if (ring >= kStages) ok = __all_sync(FULL, wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p));
+      if (ok && lane == 0) mbar_arrive(&sm.full[st]);
+      ring += ok;
     }
-  } while (w.next(a));
+  } while (ok && w.next(a));
   // every copy lands before this block's shared memory is released
   if (lane == 0)
     for (int i = max(0, ring - kStages); i < ring; ++i) mbar_drain(&sm.full[i % kStages], (i / kStages) & 1, p.wait_ns);
@@ -524,7 +521,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
 
     for (int t = wk.t_begin; t < wk.t_end; ++t, ++ring) {
       const int st = ring % kStages;
-      wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+      const bool landed = wait(sm, &sm.full[st], (ring / kStages) & 1, p);
       const uint32_t kb = smem_u32(sm.k[st]), vb = smem_u32(sm.v[st]);
       const int k0 = warp * (kTile / 4), j0 = t * kTile + k0;
       const unsigned bad_bits = (unsigned)(sm.bad[st][k0 >> 6] >> (k0 & 63)) & (kSub == 1 ? 0xffffu : FULL);
@@ -712,7 +709,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
       if (j0 < all_first || j0 + kTile / 4 > all_last || bad_bits) keys(std::true_type());
       else keys(std::false_type());
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[st]);
+      if (lane == 0 && landed) mbar_arrive(&sm.empty[st]);
     }
 
     // ---- the warps' results meet in a stage: rows of D + 4 floats ----
@@ -721,7 +718,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(FULL, l[e], d);
-    wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+    const bool landed = wait(sm, &sm.full[st], (ring / kStages) & 1, p);
     constexpr int kLd = D + 4;
     static_assert(2 * 8 * kLd * 4 <= L::kSide, "two warps' O fit one side of a stage");
     const auto scratch = [&](int w) { return reinterpret_cast<float*>(w & 2 ? sm.v[st] : sm.k[st]) + (w & 1) * 8 * kLd; };
@@ -786,7 +783,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
     }
     fence_async_shared();                                     // the stage goes back to TMA
     consumer_sync();
-    if (lane == 0) mbar_arrive(&sm.empty[st]);
+    if (lane == 0 && landed) mbar_arrive(&sm.empty[st]);
     ++ring;
     if (c0 != c1 && ends_last(sm, p, c0, c1)) join_parts<D>(sm, p, it, b, h, c0, c1);
   } while (wk.next(a));
@@ -880,7 +877,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
 
       for (int t = t_begin; t < t_end; ++t, ++ring) {
         const int st = ring % kStages;
-        wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+        const bool landed = wait(sm, &sm.full[st], (ring / kStages) & 1, p);
         const uint32_t kb = smem_u32(sm.k[st]), vb = smem_u32(sm.v[st]);
         // 16 keys from k0 on; edge: some row does not see some of them
         const auto keys16 = [&](auto edge_tag, const int k0) {
@@ -1071,7 +1068,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
           else keys16(std::false_type(), k0);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[st]);
+        if (lane == 0 && landed) mbar_arrive(&sm.empty[st]);
       }
       // ---- the row sums of the four lanes of a row, then the key groups ----
 #pragma unroll
@@ -1091,7 +1088,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
       }
       if (kKeyGroups > 1) {
         const int st = ring % kStages;
-        wait(sm, &sm.full[st], (ring / kStages) & 1, p);
+        const bool landed = wait(sm, &sm.full[st], (ring / kStages) & 1, p);
         // one side of the stage takes the O of one warp, element by element a lane; at most two give at a time
         static_assert(L::kSide >= 16 * D * 4, "");
 #pragma unroll
@@ -1129,7 +1126,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
         }
         fence_async_shared();                                  // the stage goes back to TMA
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[st]);
+        if (lane == 0 && landed) mbar_arrive(&sm.empty[st]);
         ++ring;
       }
 
@@ -1210,7 +1207,7 @@ cudaError_t launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Para
 
 }  // namespace
 
-cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned long long wait_ns, cudaStream_t st) {
+cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned long long wait_ns, int fault, cudaStream_t st) {
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.pool.num_pages * a.pool.kv_heads * a.pool.page;
   const int esz = a.pool.dtype == PISA_CACHE_E4M3 ? 1 : 2;
@@ -1235,6 +1232,7 @@ cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned lo
   // many short sequences end last (64 sequences x 24 heads of up to 4608 tokens, e4m3: 186 us with 1, 155 with 4).
   p.item_cost = whole ? -1 : esz == 1 ? 4 : 3;
   p.wait_ns = wait_ns;
+  p.fault = fault;
   if (esz == 1) return d == 64 ? launch_rows<64, true>(km, vm, p, st) : launch_rows<128, true>(km, vm, p, st);
   return d == 64 ? launch_rows<64, false>(km, vm, p, st) : launch_rows<128, false>(km, vm, p, st);
 }

@@ -27,3 +27,9 @@ def test_a_new_e4m3_pool_holds_scales_of_its_format():
 def test_other_pools_have_no_scales(dtype):
     c = PagedCache(3, 2, 2, 16, 64, dtype, device="cpu")
     assert c.k_exp is None and c.v_exp is None and bool((c.k == 0).all())
+
+
+def test_the_testing_hook_rejects_unknown_faults():
+    for fault in (1, 2, 4, -1):
+        assert C.lib().pisa_testing_set_cache_fault(fault, 0) == C.PISA_ERR_INVALID_ARG
+    assert C.lib().pisa_testing_set_cache_fault(0, 0) == C.PISA_OK
