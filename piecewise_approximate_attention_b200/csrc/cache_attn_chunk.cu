@@ -34,7 +34,9 @@
 //
 // What does not fit is computed again: a share in which a row's exponent leaves that window, or that
 // holds a value which is not finite in a tile that only some rows see (0 * NaN would reach the rows
-// that do not), is flagged and its rows are computed by the plain routine of cache_row.cuh.  V rows of
+// that do not), is flagged and its rows are computed by the plain routine of cache_row.cuh.  That takes long (256 rows of
+// 8192 keys: some tens of milliseconds), and the block's other warps wait meanwhile for longer than their limit if need
+// be: it counts from the last sign of life of the warps at it.  V rows of
 // stale slots and of missing pages are zeroed.
 #include <cfloat>
 #include <type_traits>
@@ -88,6 +90,7 @@ struct alignas(1024) Smem {
   WalkScratch<kThreads / 32> walk;
   uint32_t tmem;
   int abort;
+  unsigned long long alive;                              // when a warp that computes rows by themselves was last seen at it, ns
 };
 
 struct Params {
@@ -106,6 +109,12 @@ template <typename S>
 __device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
   return wait_for(sm, bar, parity, p.wait_ns, p.a.seqs.status);
 }
+// The same where what is waited for may itself have to wait for rows that are computed one by one: all that hangs on the
+// next item's queries.  (In every wait of the softmax's loops it costs D = 128 6 to 8%.)
+template <typename S>
+__device__ __forceinline__ bool wait_long(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
+  return wait_for(sm, bar, parity, p.wait_ns, p.a.seqs.status, &sm.alive);
+}
 
 // Bits of 32 keys from j0 on that lie in [first, last).
 __device__ __forceinline__ uint32_t range_bits(int j0, int first, int last) {
@@ -122,8 +131,8 @@ __device__ __forceinline__ float fit_of(float l, float dl) { return dl == 0.f ? 
 // bf16 with head_dim 128 is better off without the call: prompts 230 -> 220 us).
 template <typename K, int D>
 __device__ __noinline__ void row_apart(const AttnArgs& a, int b, int kvh, const float* q, int first, int last, float* m, float* l,
-                                       float* acc) {
-  row_attention<K, D>(a, b, kvh, q, first, last, m, l, acc);
+                                       float* acc, volatile unsigned long long* alive) {
+  row_attention<K, D>(a, b, kvh, q, first, last, m, l, acc, alive);
 }
 
 template <int D, bool kF8, bool kDual>
@@ -154,6 +163,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
     }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
+    sm.alive = 0;
     fence_mbar_init();
   }
   if (warp == 13) {
@@ -245,6 +255,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           }
           float sl = a.scale_log2;       // raw score -> base-2 logit
           const int t_first = w.t_begin + (kDual ? slot : 0);
+          if (t_first < w.t_end) wait_long(sm, &sm.sfull[slot], n_tile & 1, p);         // the other slot may keep the item waiting
           for (int t = t_first; t < w.t_end; t += kDual ? 2 : 1, ++n_tile) {
             const uint32_t par = n_tile & 1;
             wait(sm, &sm.sfull[slot], par, p);
@@ -433,9 +444,10 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             int f0, l0;
             visible(a, w.s.len, w.s.len - w.s.n + i, &f0, &l0);
             float mr, lr, acc[D / 32];
+            if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(&sm.alive) = globaltimer_ns();
             const int j_first = max(f0, w.t_begin * kKeys), j_last = min(l0, w.t_end * kKeys);
-            if constexpr (D == 128 && !kF8) row_attention<__nv_bfloat16, D>(a, w.b, w.h, qs, j_first, j_last, &mr, &lr, acc);
-            else row_apart<typename std::conditional<kF8, uint8_t, __nv_bfloat16>::type, D>(a, w.b, w.h, qs, j_first, j_last, &mr, &lr, acc);
+            if constexpr (D == 128 && !kF8) row_attention<__nv_bfloat16, D>(a, w.b, w.h, qs, j_first, j_last, &mr, &lr, acc, &sm.alive);
+            else row_apart<typename std::conditional<kF8, uint8_t, __nv_bfloat16>::type, D>(a, w.b, w.h, qs, j_first, j_last, &mr, &lr, acc, &sm.alive);
             __syncwarp();
             const float inv = lr == 0.f ? 0.f : 1.f / lr;
 #pragma unroll
@@ -515,7 +527,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           const int st = n_tile & 1;
           const uint32_t ph = (n_tile >> 1) & 1;
           if constexpr (!kF8) {
-            wait(sm, &sm.vfull[st], ph, p);
+            wait_long(sm, &sm.vfull[st], ph, p);
             const uint32_t* bad = sm.bad[n_tile & 3];
             if (t * kKeys < all_first || (t + 1) * kKeys > all_last || (bad[0] | bad[1] | bad[2] | bad[3])) {
               const bool there = t * kKeys + r < w.s.len && !((bad[r >> 5] >> (r & 31)) & 1u);
@@ -540,7 +552,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           } else {
 #pragma unroll 1
             for (int side = 0; side < 2; ++side) {
-              wait(sm, &sm.rawfull[side], n_tile & 1, p);
+              wait_long(sm, &sm.rawfull[side], n_tile & 1, p);
               const uint32_t* bad = sm.bad[n_tile & 3];
               const bool there = t * kKeys + r < w.s.len && !((bad[r >> 5] >> (r & 31)) & 1u);
               const int e = there ? (int)sm.raw_exp[side][r] - kExpBias : -kExpLimit;
@@ -557,7 +569,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               const __half f16 = __float2half_rn(there ? pow2(max(-24, min(kAbove, de))) : 0.f);
               const __half2 f2 = __half2half2(f16);
               // the converted stage is free
-              if (n_tile >= kStages) wait(sm, side ? &sm.vempty[st] : &sm.kempty[st], ph ^ 1u, p);
+              if (n_tile >= kStages) wait_long(sm, side ? &sm.vempty[st] : &sm.kempty[st], ph ^ 1u, p);
               uint8_t* dst = side ? sm.v[st] : sm.k[st];
               const bool edge = t * kKeys < all_first || (t + 1) * kKeys > all_last;
               bool odd = false;
@@ -642,7 +654,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             uint64_t* full = kF8 ? &sm.rawfull[side] : side ? &sm.vfull[st] : &sm.kfull[st];
             uint64_t* empty = kF8 ? &sm.rawempty[side] : side ? &sm.vempty[st] : &sm.kempty[st];
             // warps that gave up on a copy hand its stage back all the same, after they set the abort word
-            if (n_tile >= kDeep) ok = __all_sync(FULL, wait(sm, empty, (n_tile / kDeep - 1) & 1, p) && !aborted(sm));
+            if (n_tile >= kDeep) ok = __all_sync(FULL, wait_long(sm, empty, (n_tile / kDeep - 1) & 1, p) && !aborted(sm));
             if (!ok) break;
             if (p.fault && sides == 0) continue;             // a test's: the keys that never come
             if (side == 0 && lane < 4) { // the tile's missing keys, before anything of it is released
@@ -726,8 +738,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         if (w.t_begin >= w.t_end) continue;
         const int n = w.t_end - w.t_begin;
         const bool both = kDual || w.it.rows > kRows;
-        wait(sm, &sm.qfull[0], n_item0++ & 1, p);
-        if (both) wait(sm, &sm.qfull[1], n_item1++ & 1, p);
+        wait_long(sm, &sm.qfull[0], n_item0++ & 1, p);
+        if (both) wait_long(sm, &sm.qfull[1], n_item1++ & 1, p);
         if constexpr (kDual) {                     // the slots take the tiles in turn
           scores(s0, n_tile, true);
           if (n > 1) scores(s1, n_tile + 1, true);

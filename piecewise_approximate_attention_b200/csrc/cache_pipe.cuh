@@ -17,16 +17,21 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar)) : "memory");
 }
 
-// Whether the phase has completed; sm.abort: the block's abort word.
+// Whether the phase has completed; sm.abort: the block's abort word.  alive: where a warp whose work between two arrivals
+// may outlast the limit says when it was last seen at it (nullptr: there is none); the limit counts from there.
 template <typename S>
-__device__ __forceinline__ bool wait_for(S& sm, uint64_t* bar, uint32_t parity, unsigned long long limit_ns, int* status) {
+__device__ __forceinline__ bool wait_for(S& sm, uint64_t* bar, uint32_t parity, unsigned long long limit_ns, int* status,
+                                         const volatile unsigned long long* alive = nullptr) {
   if (sm100::mbar_try_wait(bar, parity)) return true;
   volatile int* abort = &sm.abort;
   const uint64_t t0 = sm100::globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (sm100::mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    if ((it & 63u) == 0u && sm100::globaltimer_ns() - t0 > limit_ns) break;
+    if ((it & 63u) == 0u) {
+      const uint64_t now = sm100::globaltimer_ns();
+      if (now - t0 > limit_ns && (!alive || (long long)(now - *alive) > (long long)limit_ns)) break;
+    }
   }
   *abort = 1;
   set_status(status, PISA_DEVERR_WAIT_TIMEOUT);

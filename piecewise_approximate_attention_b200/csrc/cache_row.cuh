@@ -3,6 +3,7 @@
 #pragma once
 
 #include "cache.cuh"
+#include "sm100.cuh"
 
 namespace pisa {
 namespace cache {
@@ -41,16 +42,18 @@ __device__ __forceinline__ void piece(const uint8_t*, uint4 u, float* x) {
 // Keys [first, last) of sequence b and key/value head kvh; q: the query row in shared memory (float).
 // For each run of 32 keys, lane j computes the logit of key j, the warp joins them into the running
 // maximum m (base 2) and sum l, and lane c adds the values to columns c, c + 32, ... of the row (acc).
-// K: element of the pool (float, bf16, uint8_t for e4m3 codes).
+// K: element of the pool (float, bf16, uint8_t for e4m3 codes).  alive: where to say every 1024 keys that the warp is at
+// work (cache_pipe.cuh), if not null.
 template <typename K, int D>
 __device__ __forceinline__ void row_attention(const AttnArgs& a, int b, int kvh, const float* q, int first, int last, float* m_out,
-                              float* l_out, float* acc) {
+                              float* l_out, float* acc, volatile unsigned long long* alive = nullptr) {
   constexpr int kPer = 16 / (int)sizeof(K), kCols = D / 32;
   const int lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
   for (int j0 = first & ~31; j0 < last; j0 += 32) {
+    if (alive && lane == 0 && (j0 & 1023) == 0) *alive = sm100::globaltimer_ns();
     const int j = j0 + lane;
     int slot = -1;
     if (j >= first && j < last) {

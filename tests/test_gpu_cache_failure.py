@@ -83,3 +83,39 @@ def test_a_long_share_ends_soon_after_its_wait(dtype, new):
     assert bool((call() == 0).all())
     assert ((lse.double() - torch.tensor(float(n)).double().log().cuda()).abs() <= 2.0 ** -18).all()
     assert cache.device_error() == (C.PISA_OK, 0)
+
+
+def test_rows_that_are_computed_by_themselves_do_not_run_into_the_limit():
+    """One value of another size in each head sends whole shares through the routine that computes row by row, for
+    longer than the waits' limit (set to 3 ms here; such an item takes more): nothing is wrong, and nothing may be
+    reported.  Two items a block, so that its other warps wait for the second one's queries meanwhile."""
+    n, new, kv, d = 8192, 200, 296, 64
+    cache = PagedCache(64, kv, kv, 128, d, "e4m3")
+    g = torch.Generator("cuda").manual_seed(3)
+    table = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(n, kv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    v[5000] *= 2.0 ** 12
+    whole = cache.sequences(table, i32(n), n, n, starts=i32(0, n))
+    cache.append(whole, k, v)
+    cache.read(whole, k, v)
+    q = torch.randn(new, kv, d, generator=g, device="cuda").bfloat16()
+    seqs = cache.sequences(table, i32(n), n, new, starts=i32(0, new))
+    torch.cuda.synchronize()
+    assert C.lib().pisa_testing_set_cache_fault(0, 3_000_000) == C.PISA_OK
+    try:
+        t = time.perf_counter()
+        o = cache.attention(seqs, q, causal=False, softmax_scale=0.125)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - t
+    finally:
+        assert C.lib().pisa_testing_set_cache_fault(0, 0) == C.PISA_OK
+    assert took > 0.006                                      # it did outlast the limit
+    assert cache.device_error() == (C.PISA_OK, 0)
+    for h in (0, 1, 147, 295):
+        s = q[:, h].double() @ k[:, h].double().T * 0.125
+        w = torch.softmax(s, -1)
+        ref, size = w @ v[:, h].double(), w @ v[:, h].double().abs()
+        # fp32 throughout: logits of at most 0.125 * 64 * 25 off by (d + 4) 2^-23 of it, sums of n terms, one rounding
+        rel = 2 * ((d + 4) * 2.0 ** -23 * 200 + 2.0 ** -21) + 2 * n * 2.0 ** -23
+        assert bool(((o[:, h].double() - ref).abs() <= size * rel * 1.01 + 2.0 ** -8 * ref.abs()).all()), h
