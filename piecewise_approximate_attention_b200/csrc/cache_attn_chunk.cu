@@ -28,9 +28,9 @@
 // one key dominates is not off by that key's rounding (frame and prompts within 1% of the times without).
 //
 // e4m3 pools: warps 8-11 turn codes into fp16 tiles in shared memory, once for both slots, as
-// code * 2^(e - E): e the row's own exponent, E the largest of the share's first tile.  That is exact
-// for e - E in [-15, 7], so scores need one factor 2^E a share and P (fp16, 11 bits) multiplies values
-// that are all in one unit.  q becomes fp16 with a power of two per row, exactly.
+// code * 2^(e - E): e the row's own exponent, E the largest of the first tile of the share that has rows other than
+// zeros.  That is exact for e - E in [-15, 7], so scores need one factor 2^E a share and P (fp16, 11 bits) multiplies
+// values that are all in one unit.  q becomes fp16 with a power of two per row, exactly.
 //
 // What does not fit is computed again: a share in which a row's exponent leaves that window, or that
 // holds a value which is not finite in a tile that only some rows see (0 * NaN would reach the rows
@@ -59,6 +59,7 @@ constexpr float kRoom = 32768.f;              // weights of a half that P (fp16 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr uint32_t kColO = 256;
 constexpr int kStages = 2;
+constexpr int kNoUnit = 1 << 20;
 constexpr int kBelow = 15, kAbove = 7;       // exponents that fp16 holds exactly around E
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -85,8 +86,7 @@ struct alignas(1024) Smem {
   uint64_t rawfull[2], rawempty[2];
   uint64_t qfull[2], sfull[2], pfull[2][2], odone[2][2], drain;
   uint32_t bad[4][4];                                    // tile of the block & 3: keys whose page is missing
-  int unit[4][2], odd[4];                                // item & 3: E of K and V; to be computed again
-  int red[4];
+  int unit[4][2], odd[4];                                // item & 3: E of K and V, kNoUnit before they are known; to be computed again
   WalkScratch<kThreads / 32> walk;
   uint32_t tmem;
   int abort;
@@ -114,6 +114,32 @@ __device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity, cons
 template <typename S>
 __device__ __forceinline__ bool wait_long(S& sm, uint64_t* bar, uint32_t parity, const Params& p) {
   return wait_for(sm, bar, parity, p.wait_ns, p.a.seqs.status, &sm.alive);
+}
+
+// E of one side of tile t: the largest exponent of its rows that are there and not zero; false if there is none.  A row
+// of zeros is stored with the smallest exponent, so only where no row has another do the codes themselves tell.  Each
+// of the four warps finds out by itself.
+template <int D, typename S>
+__device__ __forceinline__ bool first_unit(const S& sm, int side, int t, int len, const uint32_t* bad, int* unit) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t exps = reinterpret_cast<const uint32_t*>(sm.raw_exp[side])[lane];      // of rows 4 lane ... 4 lane + 3
+  int e = -kExpLimit;
+  bool any = false;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * lane + i;
+    if (t * kKeys + r >= len || ((bad[r >> 5] >> (r & 31)) & 1u)) continue;
+    const int x = (int)((exps >> (8 * i)) & 0xffu) - kExpBias;
+    e = max(e, x);
+    if (x == -kExpLimit && !any) {
+      const uint4* row = reinterpret_cast<const uint4*>(sm.raw[side] + r * D);
+      for (int c = 0; c < D / 16; ++c) any = any || ((row[c].x | row[c].y | row[c].z | row[c].w) & 0x7f7f7f7fu);
+    }
+  }
+  *unit = __reduce_max_sync(FULL, e);
+  if (*unit > -kExpLimit || __any_sync(FULL, any)) return true;
+  *unit = 0;
+  return false;
 }
 
 // Bits of 32 keys from j0 on that lie in [first, last).
@@ -254,6 +280,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             all_last = min(all_last, __shfl_xor_sync(FULL, all_last, d));
           }
           float sl = a.scale_log2;       // raw score -> base-2 logit
+          bool open = true;              // e4m3: no E yet
           const int t_first = w.t_begin + (kDual ? slot : 0);
           if (t_first < w.t_end) wait_long(sm, &sm.sfull[slot], n_tile & 1, p);         // the other slot may keep the item waiting
           for (int t = t_first; t < w.t_end; t += kDual ? 2 : 1, ++n_tile) {
@@ -261,10 +288,13 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             wait(sm, &sm.sfull[slot], par, p);
             __syncwarp();
             tc_fence_after();
-            if (kF8 && t == t_first) {
-              // kept a normal number: -inf of a masked score times 0, or a zero score times inf, would be NaN (scores
-              // that it changes the logits of are zero, or their logits below 2^-80 or past fp32 anyway)
-              sl = sm.row_scale[slot * kRows + r] * pow2(sm.unit[w.count & 3][0]);
+            if (kF8 && open) {
+              // E may come with a later tile than the first; scores before that are zero.  The factor stays a normal
+              // number: -inf of a masked score times 0, or a zero score times inf, would be NaN (scores whose logits that
+              // changes are zero, or the logits below 2^-80 or past fp32 anyway).
+              const int e = sm.unit[w.count & 3][0];
+              open = e == kNoUnit;
+              sl = sm.row_scale[slot * kRows + r] * pow2(open ? 0 : e);
               sl = fminf(fmaxf(sl, FLT_MIN), FLT_MAX);
             }
             const uint32_t* bad = sm.bad[(tile0 + t - w.t_begin) & 3];
@@ -389,7 +419,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         // they have to agree on it whatever happens, barriers depend on it)
         bool odd = *reinterpret_cast<volatile int*>(&sm.odd[w.count & 3]) != 0;
         if (kDual) odd = softmax_or(odd);
-        const float unit = kF8 ? pow2(sm.unit[w.count & 3][1]) : 1.f;      // O's
+        const int ev = kF8 ? sm.unit[w.count & 3][1] : 0;
+        const float unit = ev == kNoUnit ? 1.f : pow2(ev);                 // O's
         const bool joined = kDual && w.t_end - w.t_begin > 1 && !odd;                 // slot 1 had tiles, too
         float4* hand = reinterpret_cast<float4*>(sm.q[0]) + r;                       // [D / 4][128]
         float2* hand_ml = reinterpret_cast<float2*>(sm.row_scale);
@@ -515,14 +546,14 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       do {
         if (w.t_begin >= w.t_end) continue;
         const int it4 = w.count & 3;
-        if (r == 0) sm.odd[it4] = 0;
+        if (r == 0) sm.odd[it4] = 0, sm.unit[it4][0] = sm.unit[it4][1] = kNoUnit;
         aux_sync();
         // keys that all of the item's rows see: tiles inside need no care
         int f0, l0, f1, l1;
         visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0()), &f0, &l0);
         visible(a, w.s.len, w.s.len - w.s.n + token_of(a, w.row0() + w.it.rows - 1), &f1, &l1);
         const int all_first = max(f0, f1), all_last = min(l0, l1);
-        int eu[2] = {0, 0};              // E of K and of V
+        int eu[2] = {0, 0}, has_unit = 0;         // E of K and of V, as far as there are (bits 1 and 2): 0 before
         for (int t = w.t_begin; t < w.t_end; ++t, ++n_tile) {
           const int st = n_tile & 1;
           const uint32_t ph = (n_tile >> 1) & 1;
@@ -556,13 +587,11 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               const uint32_t* bad = sm.bad[n_tile & 3];
               const bool there = t * kKeys + r < w.s.len && !((bad[r >> 5] >> (r & 31)) & 1u);
               const int e = there ? (int)sm.raw_exp[side][r] - kExpBias : -kExpLimit;
-              if (t == w.t_begin) {      // the unit of the share: the first tile's largest exponent
-                const int mx = __reduce_max_sync(FULL, e);
-                if (lane == 0) sm.red[warp - 8] = mx;
-                aux_sync();
-                eu[side] = max(max(sm.red[0], sm.red[1]), max(sm.red[2], sm.red[3]));
-                if (r == 0) sm.unit[it4][side] = eu[side];
-                aux_sync();
+              if (!(has_unit & (1 << side))) {
+                if (first_unit<D>(sm, side, t, w.s.len, bad, &eu[side])) {
+                  has_unit |= 1 << side;
+                  if (r == 0) sm.unit[it4][side] = eu[side];
+                }
               }
               const int de = e - eu[side];
               const bool far = de > kAbove || de < -kBelow;
@@ -585,7 +614,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
                   const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&h), f2);
                   y[i] = *reinterpret_cast<const uint32_t*>(&z);
                 }
-                return (x[0] | x[1] | x[2] | x[3]) != 0u;
+                return ((x[0] | x[1] | x[2] | x[3]) & 0x7f7f7f7fu) != 0u;       // -0 is a zero, too
               };
               const auto store = [&](int c, const uint32_t* y) {
                 uint8_t* at = row + (c >> 2) * S::kHalf;

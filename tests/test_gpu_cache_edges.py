@@ -123,3 +123,62 @@ def test_a_row_that_one_late_key_dominates(dtype, new, d):
     step = torch.exp2(torch.floor(torch.log2(ref.abs())) - 7)
     bound = step / 2 + 2.0 ** -8 / 129 * 2 * c.kv64[1][0].abs().max() + 2.0 ** -18 * ref.abs()
     assert bool(((got - ref).abs() <= bound).all()), ((got - ref).abs() / bound).max()
+
+
+# ---- zeros in front of ordinary tokens (e4m3: a share's unit) ------------------------------------
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("zeros", [1, 127, 128, 130, 300, 699])
+@pytest.mark.parametrize("side,new", [("k", 70), ("v", 150), ("kv", 150), ("kv", 3), ("kv", 300)])
+def test_zero_tokens_in_front(dtype, zeros, side, new):
+    """Padding at a context's beginning: rows of zeros, +0 and -0, have no say in the scales of what follows."""
+    c = Case(dtype, 2, 1, 128, 32, [700], [new], fill=False)
+    for name in side:
+        x = getattr(c, name)[0]
+        x[:, :zeros] = 0.0
+        x[:, 5:zeros:3] = -0.0
+    stored(c).check(rows=(0, 1, new // 2, new - 1))
+    c.check(causal=False, window=500, rows=(0, 1, new // 2, new - 1))
+
+
+@pytest.mark.parametrize("new", [3, 150, 300])
+@pytest.mark.parametrize("size", [2.0 ** -58, 2.0 ** 49])
+def test_numbers_at_the_scales_ends(new, size):
+    """Rows whose scale is the smallest there is without being zeros, and rows whose scale is the largest."""
+    c = Case("e4m3", 2, 1, 64, 16, [400], [new], fill=False)
+    c.v[0] = (c.v[0].float() * size).bfloat16()
+    c.k[0] = (c.k[0].float() * size).bfloat16()
+    c.q[0] = (c.q[0].float() / size).bfloat16()
+    stored(c).check(rows=(0, 1, new // 2, new - 1))
+    c.k[0][:, :200] = 0.0
+    c.v[0][:, :130] = 0.0
+    stored(c).check(rows=(0, 1, new // 2, new - 1))
+
+
+def test_zero_tokens_in_front_cost_little():
+    """They used to send whole shares through the routine for single rows, some tens of times slower."""
+    n, new, kv, d = 4096, 256, 148, 64
+    cache = PagedCache(32, kv, kv, 128, d, "e4m3")
+    table = torch.arange(32, dtype=torch.int32, device="cuda")[None]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(n, kv, d, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(new, kv, d, device="cuda").bfloat16()
+    seqs = cache.sequences(table, i32(n), n, new, starts=i32(0, new))
+
+    def ms(zeros):
+        k[:zeros] = 0.0
+        v[:zeros] = 0.0
+        v[:zeros:2] = -0.0
+        cache.append(cache.sequences(table, i32(n), n, n, starts=i32(0, n)), k, v)
+        for _ in range(2):
+            cache.attention(seqs, q, causal=False, softmax_scale=0.125)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(4):
+            cache.attention(seqs, q, causal=False, softmax_scale=0.125)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b) / 4
+
+    plain = ms(0)
+    assert max(ms(100), ms(128), ms(500)) < 2 * plain + 0.1
+    assert cache.device_error() == (C.PISA_OK, 0)
