@@ -890,7 +890,8 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned 
   p.part_fit = p.part_o + (size_t)2 * kMaxChunkBlocks * kMaxChunkRows * d;
   // Short items of which each can have a block to itself are not cut: joining costs 3 us, a tile 2.
   const long long rows_max = (long long)a.seqs.max_new * a.group, pieces = (rows_max + kRows - 1) / kRows;
-  const bool whole = a.seqs.max_len <= 8 * kKeys && pieces * a.pool.kv_heads * a.seqs.batch <= kMaxChunkBlocks;
+  const long long span = a.window > 0 ? min((long long)a.seqs.max_len, (long long)a.window + a.seqs.max_new - 1) : a.seqs.max_len;
+  const bool whole = span <= 8 * kKeys && pieces * a.pool.kv_heads * a.seqs.batch <= kMaxChunkBlocks;
   // e4m3 tiles are not ready fast enough for two slots that each want their own (190 against 185 us at 4 x 16 heads,
   // 100 rows, 30000 keys; bf16 133 against 149, with head_dim 64 107 against 146)
   const bool dual = whole || (rows_max <= kRows && esz == 2);

@@ -77,6 +77,7 @@ struct alignas(1024) Smem {
   uint64_t full[L::kStages], empty[L::kStages];
   unsigned long long bad[L::kStages][L::kTile / 64];      // keys of the tile whose page is no page of the pool, or is not there
   long long scan[kThreads / 32], before;
+  int items[kThreads / 32], longest[kThreads / 32];
   float4 join[kConsumers * 2];               // joining the parts of an item: the groups' O, maxima and sums
   float2 join_ml[16];
   float2 ml[4][16];                          // maximum and sum of the rows that a warp hands over
@@ -88,29 +89,24 @@ struct Params {
   int* counters;             // one a block, zero between calls
   float2* part_ml;           // [2 * blocks][64]: maximum and sum of a partial result's rows
   float* part_o;             // [2 * blocks][64][D]
-  int min_share, item_cost, fault;
+  int item_cost, fault;      // what an item costs besides its tiles, in tiles
   unsigned long long wait_ns;
 };
 
-// An item's keys in tiles: tiles [t0, t0 + n) of the sequence, n = 0 for no new token.  In the line it
-// takes n places for its tiles and then p.item_cost for what it costs besides them, or one place where
-// items are not cut (p.item_cost < 0); cost = 0 if n = 0.
+// An item's keys in tiles: tiles [t0, t0 + n) of the sequence, n = 0 for no new token.
 struct Item {
   Seq s;
   int t0, n, first;             // first: the first key that any row sees
-  long long cost;
 };
 template <int kTile>
-__device__ __forceinline__ Item load_item(const AttnArgs& a, int b, int item_cost) {
+__device__ __forceinline__ Item load_item(const AttnArgs& a, int b) {
   Item it;
   it.t0 = it.n = it.first = 0;
-  it.cost = 0;
   if (!load_seq(a.seqs, b, a.q.rows, &it.s) || it.s.n == 0) return it;
   const int first = a.window > 0 ? max(0, min(it.s.len, it.s.len - it.s.n - a.window + 1)) : 0;
   it.first = first;
   it.t0 = first / kTile;
   it.n = max(1, (it.s.len + kTile - 1) / kTile - it.t0);      // an empty sequence's rows are written too
-  it.cost = item_cost < 0 ? 1 : it.n + item_cost;
   return it;
 }
 
@@ -137,18 +133,27 @@ __device__ __forceinline__ float value_at(const uint8_t* tile, int r, int c) {
 }
 
 // A block's share of the line, and where it is in it; every warp walks its own copy.
+//
+// In the line an item takes n places for its tiles and then item_cost for what it costs besides them.  Shares are at
+// least two places long, and no item is cut in more than 24 parts or so: past that, joining them costs more than the
+// shorter shares save (16 heads on 4, 8000 tokens: 13.2 us, 14.3 with 48 parts, 15.6 with 96).  Short items of which each
+// can have a block to itself are not cut, and take one place each: joining parts costs 3 us (200 tokens, 4 heads: 6.4 us
+// whole, 8.2 cut; 577 tokens: 10.3 and 8.8).  All of this goes by the lengths and the window that the device finds: the
+// caller's bound may be far above them (a captured step; 4 heads, a window of 1024 in 75600 tokens: 37.9 us by the bound, 10.1 so).
+constexpr int kMostParts = 24, kWholeTiles = 6, kWholeItems = 148;
 template <int kTile>
 struct FewWalk {
   long long u0, u1, share, item0;     // places: this block's, how long shares are, the item's first
-  int b, h, t_begin, t_end, item_cost;
+  int b, h, t_begin, t_end, item_cost;      // item_cost < 0: items are not cut
   Item it;
+
+  __device__ __forceinline__ int cost(int tiles) const { return tiles == 0 ? 0 : item_cost < 0 ? 1 : tiles + item_cost; }
 
   // Whole block; false if the line ends before this block's share.
   template <typename S>
-  __device__ __forceinline__ bool start(const AttnArgs& a, S& sm, int cost_of_item, int min_share) {
+  __device__ __forceinline__ bool start(const AttnArgs& a, S& sm, int cost_of_item) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    item_cost = cost_of_item;
-    const auto places = [&](int b) { return b < a.seqs.batch ? load_item<kTile>(a, b, item_cost).cost * a.pool.kv_heads : 0LL; };
+    const auto tiles = [&](int b) { return b < a.seqs.batch ? load_item<kTile>(a, b).n : 0; };
     const auto scan = [&](long long n) {
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -157,30 +162,50 @@ struct FewWalk {
       }
       return n;
     };
-    long long total = 0, before = 0;
+    long long before = 0;
     if (a.seqs.batch <= 32) {         // each warp by itself
-      const long long n = places(lane), upto = scan(n);
-      total = __shfl_sync(FULL, upto, 31);
-      shares(total, min_share);
+      const int mine = tiles(lane);
+      const int longest = __reduce_max_sync(FULL, mine);
+      choose(a, longest, cost_of_item);
+      const long long n = (long long)cost(mine) * a.pool.kv_heads, upto = scan(n);
+      shares(__shfl_sync(FULL, upto, 31), longest);
       if (u0 >= u1) return false;
       const int w = __ffs(__ballot_sync(FULL, upto > u0)) - 1;
       b = w;
       before = __shfl_sync(FULL, upto - n, w);
     } else {
-      for (int i = threadIdx.x; i < a.seqs.batch; i += kThreads) total += places(i);
+      long long total = 0;
+      int items = 0, longest = 0;
+      for (int i = threadIdx.x; i < a.seqs.batch; i += kThreads) {
+        const int n = tiles(i);
+        total += n;
+        items += n > 0;
+        longest = max(longest, n);
+      }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(FULL, total, d);
-      if (lane == 0) sm.scan[warp] = total;
+      items = __reduce_add_sync(FULL, items);
+      longest = __reduce_max_sync(FULL, longest);
+      if (lane == 0) {
+        sm.scan[warp] = total;
+        sm.items[warp] = items;
+        sm.longest[warp] = longest;
+      }
       __syncthreads();
-      total = 0;
+      total = items = longest = 0;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) total += sm.scan[w];
-      shares(total, min_share);
+      for (int w = 0; w < kThreads / 32; ++w) {
+        total += sm.scan[w];
+        items += sm.items[w];
+        longest = max(longest, sm.longest[w]);
+      }
+      choose(a, longest, cost_of_item);
+      shares((item_cost < 0 ? items : total + (long long)items * item_cost) * a.pool.kv_heads, longest);
       if (u0 >= u1) return false;
       if (warp == 0) {                // 32 sequences at a time
         long long base = 0;
         for (int b0 = 0; b0 < a.seqs.batch; b0 += 32) {
-          const long long n = places(b0 + lane), upto = scan(n);
+          const long long n = (long long)cost(tiles(b0 + lane)) * a.pool.kv_heads, upto = scan(n);
           const unsigned hit = __ballot_sync(FULL, base + upto > u0);
           if (hit) {
             const int w = __ffs(hit) - 1;
@@ -197,14 +222,18 @@ struct FewWalk {
       b = sm.start_b;
       before = sm.before;
     }
-    it = load_item<kTile>(a, b, item_cost);
-    h = (int)quotient(u0 - before, it.cost);
-    item0 = before + h * it.cost;
+    it = load_item<kTile>(a, b);
+    h = (int)quotient(u0 - before, cost(it.n));
+    item0 = before + (long long)h * cost(it.n);
     enter();
     return true;
   }
-  __device__ __forceinline__ void shares(long long total, int min_share) {
-    share = max((long long)min_share, quotient(total + gridDim.x - 1, gridDim.x));
+  __device__ __forceinline__ void choose(const AttnArgs& a, int longest, int cost_of_item) {
+    item_cost = longest <= kWholeTiles && (long long)a.seqs.batch * a.pool.kv_heads <= kWholeItems ? -1 : cost_of_item;
+  }
+  __device__ __forceinline__ void shares(long long total, int longest) {
+    const int least = item_cost < 0 ? 1 : max(2, (longest + kMostParts - 1) / kMostParts);
+    share = max((long long)least, quotient(total + gridDim.x - 1, gridDim.x));
     u0 = share * blockIdx.x;
     u1 = min(total, u0 + share);
   }
@@ -219,11 +248,11 @@ struct FewWalk {
     t_end = it.t0 + (int)min((long long)it.n, u1 - item0);
   }
   __device__ __forceinline__ bool next(const AttnArgs& a) {
-    item0 += it.cost;
+    item0 += cost(it.n);
     if (item0 >= u1) return false;
     if (++h == a.pool.kv_heads) {
       h = 0;
-      do it = load_item<kTile>(a, ++b, item_cost); while (it.n == 0);   // the line goes on: there is one
+      do it = load_item<kTile>(a, ++b); while (it.n == 0);   // the line goes on: there is one
     }
     enter();
     return true;
@@ -312,7 +341,7 @@ __device__ __forceinline__ bool set_up(S& sm, const Params& p, FewWalk<Layout<D,
   }
   griddep_launch_dependents();
   griddep_wait();
-  const bool any = w.start(p.a, sm, p.item_cost, p.min_share);
+  const bool any = w.start(p.a, sm, p.item_cost);
   __syncthreads();
   return any;
 }
@@ -1188,11 +1217,11 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
     else return attn_few<D, kF8, MT>;
   }();
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem))) return e;
-  // no more blocks than there can be tiles
+  // no more blocks than there can be places
   constexpr int kTile = Layout<D, kF8>::kTile;
-  const long long tiles = (long long)p.a.seqs.batch * p.a.pool.kv_heads *
-                          (p.item_cost < 0 ? 1 : (p.a.seqs.max_len + kTile - 1) / kTile + 1 + p.item_cost);
-  const int blocks = (int)min((long long)min(2 * sms, kMaxFewBlocks), tiles);
+  const long long items = (long long)p.a.seqs.batch * p.a.pool.kv_heads, tiles = ((long long)p.a.seqs.max_len + kTile - 1) / kTile;
+  const long long places = tiles <= kWholeTiles && items <= kWholeItems ? items : items * (tiles + 1 + p.item_cost);
+  const int blocks = (int)min((long long)min(2 * sms, kMaxFewBlocks), places);
   return launch_after(kernel, dim3(blocks), kThreads, smem, st, km, vm, p);
 }
 
@@ -1221,16 +1250,9 @@ cudaError_t launch_attention_few(const AttnArgs& a, int d, void* ws, unsigned lo
   p.counters = reinterpret_cast<int*>(w + kCountersAt);
   p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxFewBlocks * kMaxFewRows);
-  // Shares of at least two places, and no item in more than 24 parts or so: past that, joining them costs more than
-  // the shorter shares save (16 heads on 4, 8000 tokens: 13.2 us, 14.3 with 48 parts, 15.6 with 96).
-  const long long tiles = (a.seqs.max_len + tile - 1) / tile, items = (long long)a.seqs.batch * a.pool.kv_heads;
-  // Short items of which each can have a block to itself are not cut: joining parts costs 3 us (200 tokens, 4 heads:
-  // 6.4 us whole, 8.2 cut; 577 tokens: 10.3 and 8.8).
-  const bool whole = tiles <= 6 && items <= 148;
-  p.min_share = whole ? 1 : max(2, ((a.seqs.max_len + tile - 1) / tile + 23) / 24);
   // What an item costs besides its tiles (queries, the warps' join, output), in tiles: without it the blocks with
   // many short sequences end last (64 sequences x 24 heads of up to 4608 tokens, e4m3: 186 us with 1, 155 with 4).
-  p.item_cost = whole ? -1 : esz == 1 ? 4 : 3;
+  p.item_cost = esz == 1 ? 4 : 3;
   p.wait_ns = wait_ns;
   p.fault = fault;
   if (esz == 1) return d == 64 ? launch_rows<64, true>(km, vm, p, st) : launch_rows<128, true>(km, vm, p, st);

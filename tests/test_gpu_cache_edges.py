@@ -182,3 +182,47 @@ def test_zero_tokens_in_front_cost_little():
     plain = ms(0)
     assert max(ms(100), ms(128), ms(500)) < 2 * plain + 0.1
     assert cache.device_error() == (C.PISA_OK, 0)
+
+
+# ---- bounds far above what is there --------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ("bf16", "e4m3"))
+@pytest.mark.parametrize("new", [1, 3, 12, 30])
+@pytest.mark.parametrize("lens", [[577], [1300, 90], [200], [900] * 40])
+def test_the_bound_of_the_lengths_does_not_change_how_work_is_shared(dtype, new, lens):
+    """As a captured step has it, sized for the longest context there may be: the parts that are joined, and so the
+    bits, are those of a call with the bound at the lengths.  So for up to 64 rows a key/value head; above, the kernel's
+    form is chosen on the host, which has the bound alone, and both results are held to their definition."""
+    c = Case(dtype, 8, 2, 128, 32, lens, [new] * len(lens))
+    q = c.tokens(c.q, 8).cuda()
+    table = torch.full((len(lens), 2400), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.max_pages] = c.table.cuda()
+    loose = c.cache.sequences(table, c.seqs.tensors[1], max_len=75600, max_new=new, starts=c.seqs.tensors[2])
+    got = []
+    for seqs in (c.seqs, loose):
+        lse = torch.empty(q.shape[:-1], device="cuda")
+        got.append((c.cache.attention(seqs, q, softmax_scale=c.scale, lse=lse), lse))
+    if 4 * new <= 64:
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    else:
+        c.check(rows=(0, new - 1))
+        c.seqs = loose
+        c.check(rows=(0, new - 1))
+    assert c.cache.device_error() == (C.PISA_OK, 0)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "e4m3"))
+@pytest.mark.parametrize("new", [1, 3, 12, 30])
+def test_what_lies_behind_a_window_does_not_change_how_work_is_shared(dtype, new):
+    """A window over a long context is shared out like the same window over its last pages alone."""
+    n, last = 20_000, 20_000 - 16_384              # the same place in a tile
+    c = Case(dtype, 8, 2, 128, 128, [n], [new])
+    q = c.tokens(c.q, 8).cuda()
+    tail = c.table[:, 128:].contiguous().cuda()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    short = c.cache.sequences(tail, i32(last), max_len=last, max_new=new, starts=i32(0, new))
+    got = []
+    for seqs in (c.seqs, short):
+        lse = torch.empty(q.shape[:-1], device="cuda")
+        got.append((c.cache.attention(seqs, q, window=1024, softmax_scale=c.scale, lse=lse), lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    c.check(window=1024, rows=(0, new - 1))
