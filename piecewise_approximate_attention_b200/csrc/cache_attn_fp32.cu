@@ -753,8 +753,8 @@ cudaError_t launch_few(const Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const size_t smem = sizeof(Smem<D>);
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_few<D>), smem))) return e;
-  const int per_sm = smem <= 113 * 1024 ? 2 : 1;
-  return launch_after(attn_few<D>, dim3(min(per_sm * sms, kMaxFewBlocks)), kThreads, smem, st, p);
+  static_assert(sizeof(Smem<D>) <= 113 * 1024, "two blocks' shared memory fits an SM");
+  return launch_after(attn_few<D>, dim3(min(2 * sms, kMaxFewBlocks)), kThreads, smem, st, p);
 }
 
 template <int D>
