@@ -112,6 +112,16 @@ class Pisa:
         return C.pisa_read_device_error(self.ws, stream)
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _int32(name: str, x: int) -> int:
+    """ctypes would cut what does not fit."""
+    if not 0 <= x <= _INT32_MAX:
+        raise ValueError(f"{name} must lie in [0, 2^31), not be {x}")
+    return x
+
+
 class Sequences:
     """Which tokens a call on a PagedCache is about; made by PagedCache.sequences, reusable for any
     number of calls (every layer of a step) while its tensors hold what is meant."""
@@ -141,6 +151,8 @@ class PagedCache:
             raise ValueError(f"dtype must be one of {sorted(self.DTYPES)}")
         if heads < 1 or kv_heads < 1 or heads % kv_heads:
             raise ValueError("heads must be a multiple of kv_heads")
+        for name, x in (("num_pages", num_pages), ("heads", heads), ("page", page), ("head_dim", head_dim)):
+            _int32(name, x)
         self.num_pages, self.heads, self.kv_heads, self.page, self.head_dim = num_pages, heads, kv_heads, page, head_dim
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
@@ -186,7 +198,7 @@ class PagedCache:
                 raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} axes and {n} rows on {self.device}")
         if starts is not None and counts is not None:
             raise ValueError("starts (packed) and counts (padded) exclude one another")
-        c = C.PisaSequences(batch, page_table.shape[1], max_len, max_new, C._ptr(page_table), C._ptr(lens),
+        c = C.PisaSequences(batch, page_table.shape[1], _int32("max_len", max_len), _int32("max_new", max_new), C._ptr(page_table), C._ptr(lens),
                             C._ptr(starts), C._ptr(counts))
         return Sequences(c, starts is not None, batch, (page_table, lens, starts, counts))
 
@@ -228,7 +240,7 @@ class PagedCache:
     def attention(self, seqs: Sequences, q, o=None, causal: bool = True, window: int = 0, softmax_scale: float = 1.0,
                   lse=None, stream=None):
         """Attention of the new tokens' q (heads heads) over their sequence's cached tokens, into o.
-        ``causal``: no later token is seen; ``window`` > 0: only keys less than that far back.  ``lse``
+        ``causal``: no later token is seen; ``window`` > 0: only keys less than that far back (of any size).  ``lse``
         (fp32, [tokens, heads] packed or [batch, heads, rows] padded) takes the log of the softmax sum."""
         if o is None:                    # rows that belong to no token are zero in a tensor made here
             import torch
@@ -241,7 +253,8 @@ class PagedCache:
             shape = q.shape[:-1]
             if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous() or lse.device != self.device:
                 raise ValueError(f"lse must be a contiguous float32 tensor {tuple(shape)} on {self.device}")
-        self._call(C.pisa_cache_attention, (self.c, seqs.c, self.heads, bool(causal), int(window), softmax_scale,
+        window = max(-1, min(int(window), _INT32_MAX))
+        self._call(C.pisa_cache_attention, (self.c, seqs.c, self.heads, bool(causal), window, softmax_scale,
                                             self._rows(seqs, q, self.heads, "q"),
                                             self._rows(seqs, o, self.heads, "o"), lse), stream)
         return o
