@@ -215,12 +215,15 @@ class PagedCache:
             return C.PisaRows(x.data_ptr(), shape[0], 0, strides[0], strides[1])
         return C.PisaRows(x.data_ptr(), shape[2], strides[0], strides[2], strides[1])
 
+    def _device_index(self) -> int:
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache is on {self.device}: the kernels take CUDA tensors only")
+        return self.device.index
+
     def _call(self, fn, args, stream):
         """On the cache's device, whatever the current one is."""
         import torch
-        if self.device.type != "cuda":
-            raise ValueError(f"the cache is on {self.device}: the kernels take CUDA tensors only")
-        index = self.device.index
+        index = self._device_index()
         if index == torch.cuda.current_device():
             fn(*args, self._ws_at, self._ws_bytes, C.stream_handle(stream, index))
         else:
@@ -260,7 +263,10 @@ class PagedCache:
         return o
 
     def device_error(self, stream=None):
-        return C.pisa_read_device_error(self.ws, stream)
+        """(status, code) of the calls so far on ``stream`` (the current one of the cache's device if None); clears it."""
+        import torch
+        with torch.cuda.device(self._device_index()):
+            return C.pisa_read_device_error(self.ws, stream)
 
 
 AXIS_ORDERS = ("thw", "twh", "htw", "hwt", "wth", "wht")

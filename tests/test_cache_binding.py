@@ -85,3 +85,13 @@ def test_a_window_of_any_size_means_what_it_says(monkeypatch, window, reaches):
     seen = _calls(monkeypatch, c)
     c.attention(seqs, q, torch.zeros_like(q), window=window)
     assert seen[0][1][4] == reaches
+
+
+def test_the_status_is_read_on_the_cache_s_device(monkeypatch):
+    """Whatever the current one is: its stream orders the read after the cache's calls."""
+    c = PagedCache(4, 2, 2, 16, 64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        c.device_error()
+    seen = _calls(monkeypatch, c)
+    assert c.device_error() == (0, 0) and c.device_error("a stream") == (0, 0)
+    assert seen == [(1, None), (1, "a stream")]
