@@ -55,6 +55,10 @@ constexpr int kKeys = 128;                   // keys of a tile
 constexpr int kRows = 128;                   // rows of a slot
 constexpr int kThreads = 512;
 constexpr float kPart = 0.5f;                // bf16 pools; 0.125 costs prompts 7%: their shares are short, most of their halves bring that much
+// e4m3 pools: weights reach 2^8 where the maximum is moved, so those that are normal fp16 numbers reach down to 2^-22 of a
+// row's largest, and what is lost below is at most 2^-33 of it a key: many small weights can matter beside a large one
+// whose values are small.
+template <bool kF8> constexpr float kLift = kF8 ? 8.f : 0.f;
 constexpr float kRoom = 32768.f;              // weights of a half that P (fp16 at least) takes as they are
 constexpr unsigned FULL = 0xffffffffu;
 constexpr uint32_t kColO = 256;
@@ -374,7 +378,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
                 const float top = largest();
                 if (__any_sync(FULL, first_half || ls > kRoom || m == -INFINITY)) {
                   // rare but for the first half: move the maximum, and with it l and O
-                  const float m_new = fmaxf(m, top * sl);                            // base-2 units
+                  const float m_new = fmaxf(m, top * sl - kLift<kF8>);               // base-2 units
                   const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);         // 0 when m = -inf
                   l *= f;
                   if (!kF8) *dl *= f;

@@ -226,3 +226,29 @@ def test_what_lies_behind_a_window_does_not_change_how_work_is_shared(dtype, new
         got.append((c.cache.attention(seqs, q, window=1024, softmax_scale=c.scale, lse=lse), lse))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     c.check(window=1024, rows=(0, new - 1))
+
+
+# ---- weights far below a row's largest -----------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 5, 20, 60, 70, 100, 150, 300])
+def test_many_small_weights_beside_a_large_one_of_small_values(new, d):
+    """e4m3: one key takes nearly all the weight, with values 2^-14 of the others', whose weights of 2^-22.6 make up most
+    of the result.  The bounds of cache_reference, with what falls below fp16's normal range counted from weights that
+    reach 2^8: half a step of 2^-24 over 2^8 a key, 2^-33 of the largest |v|."""
+    n = 2000
+    c = Case("e4m3", 1, 1, d, 32, [n], [new], scale=math.log(2.0), fill=False)
+    c.q[0] = torch.ones_like(c.q[0])
+    c.k[0] = torch.full_like(c.k[0], 0.0)
+    c.k[0][0, 1:, 0] = -20.0
+    c.k[0][0, 1:, 1] = -2.5
+    c.k[0][0, 1:, 2] = -0.1015625                # -22.6
+    c.v[0] = (c.v[0].float().abs() * 0.25 + 1.0).bfloat16()
+    c.v[0][0, 0] = 2.0 ** -14
+    stored(c)
+    got = c.split(c.cache.attention(c.seqs, c.tokens(c.q, 1).cuda(), causal=False, softmax_scale=c.scale))[0][0].double()
+    ref = R.attention(c.q[0][0].double(), c.kv64[0][0][0], c.kv64[1][0][0], list(range(n - new, n)), False, 0,
+                      float(torch.tensor(c.scale, dtype=torch.float32)))
+    rel = 2.0 ** -11 + 2 * ((d + 4) * 2.0 ** -23 * ref["size"] + 2.0 ** -21) + 2 * ref["seen"] * 2.0 ** -23
+    bound = ref["mean_abs"] * rel[:, None] * 1.01 + 2.0 ** -8 * ref["o"].abs() + n * 2.0 ** -33 * ref["vmax"]
+    err = (got - ref["o"]).abs()
+    assert bool((err <= bound).all()), (err / ref["o"].abs()).max()
