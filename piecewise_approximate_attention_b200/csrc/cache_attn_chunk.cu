@@ -25,7 +25,9 @@
 // (frame of 1560 tokens 399 -> 608 us, prompts 210 -> 319), a sum of all weights as rounded beside theirs 20%.  What is
 // done: a half that brings kPart of what a row has so far, or more, notes by how much its largest weight was
 // rounded, and the share's O is scaled by the sum of the weights over the sum with that rounding, so that a row which
-// one key dominates is not off by that key's rounding (frame and prompts within 1% of the times without).
+// one key dominates is not off by that key's rounding (frame and prompts within 1% of the times without).  Where one key
+// holds the weight and others, of far larger values, the result, its rounding and theirs may add up, to 2^-7.  (Adding
+// what was left of the largest weight times its value to O instead: prompts +5 to 16%, 70 tokens in a window +8 to 25%.)
 //
 // e4m3 pools: warps 8-11 turn codes into fp16 tiles in shared memory, once for both slots, as
 // code * 2^(e - E): e the row's own exponent, E the largest of the first tile of the share that has rows other than

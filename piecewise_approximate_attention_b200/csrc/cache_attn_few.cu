@@ -30,13 +30,15 @@
 // float64 falls from 2.35e-3, the output's rounding and the weights', to 1.67e-3, the output's alone).  Above, where
 // the second product would cost 23% (30 rows) to 38% (60), weights are bf16, off by 2^-8 at most, and O is scaled by
 // the sum of the weights over the sum of the rounded ones, so that a row which one key dominates is not off by
-// that key's rounding (3% at 60 rows).  Sums are of the weights themselves.
+// that key's rounding (3% at 60 rows; second parts for the steps that count: 14 to 29%).  Where one key holds the weight
+// and others, of far larger values, the result, its rounding and theirs may add up, to 2^-7.  Sums are of the weights themselves.
 //
 // e4m3 pools: codes become fp16 exactly (one instruction for two), q becomes fp16 with a power of
 // two per row, also exactly, and a key's scales act on the logits: with x_j = s_j + e_j (e_j the
 // exponent of v_j's scale, in base-2 logits) the weight of code row j is 2^(x_j - M), M the maximum of
 // the x, and the sum takes 2^(x_j - M) 2^-e_j.  So the fp16 weights keep 11 bits for what counts most
-// in O, however the rows' scales differ.
+// in O, however the rows' scales differ.  (x_j is rounded like a number of e_j's size, so a log-sum-exp is off by up to
+// 2^-18 where scales are as far from 1 as they may be.)
 //
 // Positions that a row does not see get weight zero; the V rows behind the last position (stale
 // slots) are zeroed in registers, because 0 * NaN is NaN, and a value that is not finite where only
