@@ -139,7 +139,7 @@ constexpr int kMaxChunkBlocks = 148, kMaxChunkRows = 256;  // chunk attention: o
 constexpr size_t kPartialsAt = kSplitAt + (kMaxChunkBlocks * sizeof(int4) + 255) / 256 * 256;
 inline size_t partials_bytes(int d) {
   const size_t few = (size_t)kMaxFewBlocks * kMaxFewRows, chunk = (size_t)kMaxChunkBlocks * kMaxChunkRows;
-  return 2 * (few > chunk ? few : chunk) * (d + 3) * sizeof(float);
+  return 2 * (few > chunk ? few : chunk) * (d + 2) * sizeof(float);
 }
 
 // Launches a kernel that may be scheduled while the one before it in the stream still runs

@@ -22,12 +22,9 @@
 // bf16 pools: K and V are used as stored; P is bf16, as the type of V asks of the MMA (each weight is
 // off by 2^-8 at most, like the output's own rounding; the error against float64 is 2.33e-3 where the output's rounding
 // alone is 1.66e-3).  Weights in two bf16 parts, as cache_attn_few.cu has them for few rows, would take half as long again
-// (frame of 1560 tokens 399 -> 608 us, prompts 210 -> 319), a sum of all weights as rounded beside theirs 20%.  What is
-// done: a half that brings kPart of what a row has so far, or more, notes by how much its largest weight was
-// rounded, and the share's O is scaled by the sum of the weights over the sum with that rounding, so that a row which
-// one key dominates is not off by that key's rounding (frame and prompts within 1% of the times without).  Where one key
-// holds the weight and others, of far larger values, the result, its rounding and theirs may add up, to 2^-7.  (Adding
-// what was left of the largest weight times its value to O instead: prompts +5 to 16%, 70 tokens in a window +8 to 25%.)
+// (frame of 1560 tokens 399 -> 608 us, prompts 210 -> 319).  What is done: the maximum is also moved where a half outweighs
+// kPart times all that its row has so far, so that a key which holds four fifths of a row or more weighs exactly 1 and
+// such a row is not off by its rounding (frame +1%, prompts +3%).
 //
 // e4m3 pools: warps 8-11 turn codes into fp16 tiles in shared memory, once for both slots, as
 // code * 2^(e - E): e the row's own exponent, E the largest of the first tile of the share that has rows other than
@@ -56,7 +53,7 @@ using namespace sm100;
 constexpr int kKeys = 128;                   // keys of a tile
 constexpr int kRows = 128;                   // rows of a slot
 constexpr int kThreads = 512;
-constexpr float kPart = 0.5f;                // bf16 pools; 0.125 costs prompts 7%: their shares are short, most of their halves bring that much
+constexpr float kPart = 4.f;                  // bf16 pools: see above
 // e4m3 pools: weights reach 2^8 where the maximum is moved, so those that are normal fp16 numbers reach down to 2^-22 of a
 // row's largest, and what is lost below is at most 2^-33 of it a key: many small weights can matter beside a large one
 // whose values are small.
@@ -87,7 +84,6 @@ struct alignas(1024) Smem {
   uint8_t raw[kF8 ? 2 : 1][kF8 ? kKeys * D : 16];        // e4m3 codes as loaded, K and V in turn
   uint8_t raw_exp[2][kKeys];
   float row_scale[2 * kRows];                            // raw score -> base-2 logit, but for 2^E; at an item's end slot 1's (maximum, sum)
-  float rounded[kF8 ? 1 : 2 * kRows];                    // bf16: sum of the roundings of weights that may dominate their row
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], vready[kStages];
   uint64_t rawfull[2], rawempty[2];
   uint64_t qfull[2], sfull[2], pfull[2][2], odone[2][2], drain;
@@ -103,7 +99,6 @@ struct Params {
   AttnArgs a;
   int4* split;               // one a block: the item that begins in it and is shared (sequence, head, pair, parts), parts = 0 for none
   float2* part_ml;           // [2 * blocks][256]
-  float* part_fit;           // [2 * blocks][256], bf16 pools
   float* part_o;             // [2 * blocks][D / 4][256][4]: a warp's rows next to one another
   int log_rows;              // rows of an item: 2^7 or 2^8
   int item_cost;             // what an item costs besides its tiles, in tiles; < 0: items are not cut (cache_walk.cuh)
@@ -155,9 +150,6 @@ __device__ __forceinline__ uint32_t range_bits(int j0, int first, int last) {
   if (lo > 0) m &= lo >= 32 ? 0u : ~((1u << lo) - 1u);
   return m;
 }
-
-// What O is scaled by where its weights were rounded by dl in all, for a sum of l.
-__device__ __forceinline__ float fit_of(float l, float dl) { return dl == 0.f ? 1.f : l / (l + dl); }
 
 // Out of line, the rare path's registers stay out of the softmax's (frame of 1560 tokens, head_dim 64: 389 -> 362 us;
 // bf16 with head_dim 128 is better off without the call: prompts 230 -> 220 us).
@@ -224,8 +216,6 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         const bool valid = row < w.it.rows;
         const int tok = valid ? token_of(a, grow_) : 0, head = w.h * a.group + (valid ? grow_ - tok * a.group : 0);
         float m = -INFINITY, l = 0.f;
-        float* dl = &sm.rounded[kF8 ? 0 : slot * kRows + r];         // the row's: in a register it costs the loop 10%
-        if (!kF8) *dl = 0.f;
         int first = 0, last = w.s.len;
         if (valid) visible(a, w.s.len, w.s.len - w.s.n + tok, &first, &last);
         if (active) {
@@ -375,37 +365,29 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               };
               const bool first_half = t == t_first && hh == 0;
               if (!first_half) weights();
-              // bf16: no weight yet, or one that may dominate, or one that does not fit (NaN sums too)
+              // bf16: no weight yet, or one that may dominate the row, or one that does not fit (NaN sums too)
               if (__any_sync(FULL, kF8 ? first_half || ls > kRoom || m == -INFINITY : !(ls < fminf(kRoom, kPart * l)))) {
-                const float top = largest();
-                if (__any_sync(FULL, first_half || ls > kRoom || m == -INFINITY)) {
-                  // rare but for the first half: move the maximum, and with it l and O
-                  const float m_new = fmaxf(m, top * sl - kLift<kF8>);               // base-2 units
-                  const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);         // 0 when m = -inf
-                  l *= f;
-                  if (!kF8) *dl *= f;
-                  m = m_new;
-                  if (!first_half) {
-                    // O holds the products of the halves before this one
-                    wait(sm, &sm.odone[slot][hh ^ 1], hh ? par : par ^ 1u, p);
-                    __syncwarp();
-                    tc_fence_after();
+                // rare but for the first half: move the maximum, and with it l and O
+                const float m_new = fmaxf(m, largest() * sl - kLift<kF8>);         // base-2 units
+                const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);         // 0 when m = -inf
+                l *= f;
+                m = m_new;
+                if (!first_half) {
+                  // O holds the products of the halves before this one
+                  wait(sm, &sm.odone[slot][hh ^ 1], hh ? par : par ^ 1u, p);
+                  __syncwarp();
+                  tc_fence_after();
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                      float ov[16];
-                      tmem_ld16(to + 16 * ch, ov);
-                      tmem_ld_wait();
+                  for (int ch = 0; ch < D / 16; ++ch) {
+                    float ov[16];
+                    tmem_ld16(to + 16 * ch, ov);
+                    tmem_ld_wait();
 #pragma unroll
-                      for (int x = 0; x < 16; ++x) ov[x] *= f;
-                      tmem_st16(to + 16 * ch, reinterpret_cast<const uint32_t*>(ov));
-                    }
+                    for (int x = 0; x < 16; ++x) ov[x] *= f;
+                    tmem_st16(to + 16 * ch, reinterpret_cast<const uint32_t*>(ov));
                   }
-                  weights();
                 }
-                if constexpr (!kF8) {
-                  const float w0 = ex2(fmaf(top, sl, m == -INFINITY ? 0.f : -m));    // as in weights()
-                  *dl += __uint_as_float(pack_bf16x2(w0, w0) << 16) - w0;
-                }
+                weights();
               }
               l += ls;
               tmem_st_wait();
@@ -448,16 +430,11 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           softmax_sync();
           if (slot == 0) {
             const float2 o = hand_ml[r];
-            const float l_own = l;
             const float mn = fmaxf(m, o.x), base = mn == -INFINITY ? 0.f : mn;
             f_own = ex2(m - base);
             f_other = ex2(o.x - base);
             m = mn;
             l = l * f_own + o.y * f_other;
-            if (!kF8) {
-              f_own *= fit_of(l_own, dl[0]);
-              f_other *= fit_of(o.y, dl[kRows]);
-            }
           }
         }
         const bool writes = kDual ? slot == 0 : active;
@@ -494,14 +471,12 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             }
             if (lane == 0) {
               float* lse = lse_at(a, w.b, w.s, i, hh);
-              if (c0 != c1) {
-                p.part_ml[part + ir] = make_float2(mr, lr);
-                if (!kF8) p.part_fit[part + ir] = 1.f;
-              } else if (lse) *lse = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
+              if (c0 != c1) p.part_ml[part + ir] = make_float2(mr, lr);
+              else if (lse) *lse = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
             }
           }
         } else if (writes) {
-          const float lr = kF8 || joined ? l : l + *dl, inv = (lr == 0.f ? 0.f : 1.f / lr) * unit;
+          const float inv = (l == 0.f ? 0.f : 1.f / l) * unit;
 #pragma unroll
           for (int ch = 0; ch < D / 32; ++ch) {
             float ov[32];
@@ -533,10 +508,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
             }
           }
           if (valid) {
-            if (c0 != c1) {
-              p.part_ml[part + row] = make_float2(m, l);
-              if (!kF8) p.part_fit[part + row] = joined ? 1.f : fit_of(l, *dl);
-            } else if (float* lse = lse_at(a, w.b, w.s, tok, head)) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            if (c0 != c1) p.part_ml[part + row] = make_float2(m, l);
+            else if (float* lse = lse_at(a, w.b, w.s, tok, head)) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
           }
           tc_fence_before();             // O is read before the next item's first product overwrites it
         }
@@ -820,7 +793,7 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
 // Joins the parts of the items that several blocks worked on.  Block (i, y): the item that begins in
 // block i of the attention kernel, its rows [64 y, 64 y + 64), a warp 8 of them, a lane four columns of
 // one row at a time.
-template <int D, bool kF8>
+template <int D>
 __global__ void __launch_bounds__(256) attn_join(const Params p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -843,10 +816,9 @@ __global__ void __launch_bounds__(256) attn_join(const Params p) {
 #pragma unroll 2
   for (int x = 0; x < parts; ++x) {
     const float2 ml = p.part_ml[slot_of(x) + r];
-    float f = ex2(ml.x - base);
+    const float f = ex2(ml.x - base);
     const float4* src = reinterpret_cast<const float4*>(p.part_o + slot_of(x) * D) + (lane >> 3) * kMaxChunkRows + r;
     l = fmaf(ml.y, f, l);
-    if (!kF8) f *= p.part_fit[slot_of(x) + r];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       const float4 v = src[4 * c * kMaxChunkRows];
@@ -876,7 +848,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& p
   const int blocks = min(sms, kMaxChunkBlocks);
   if ((e = launch_after(attn_chunk<D, kF8, kDual>, dim3(blocks), kThreads, smem, st, km, vm, p)) != cudaSuccess) return e;
   if (p.item_cost < 0) return cudaSuccess;      // no item is cut
-  return launch_after(attn_join<D, kF8>, dim3(blocks, kMaxChunkRows / 64), 256, 0, st, p);
+  return launch_after(attn_join<D>, dim3(blocks, kMaxChunkRows / 64), 256, 0, st, p);
 }
 
 }  // namespace
@@ -893,7 +865,6 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, int d, void* ws, unsigned 
   p.split = reinterpret_cast<int4*>(w + kSplitAt);
   p.part_ml = reinterpret_cast<float2*>(w + kPartialsAt);
   p.part_o = reinterpret_cast<float*>(w + kPartialsAt + sizeof(float2) * 2 * kMaxChunkBlocks * kMaxChunkRows);
-  p.part_fit = p.part_o + (size_t)2 * kMaxChunkBlocks * kMaxChunkRows * d;
   // Short items of which each can have a block to itself are not cut: joining costs 3 us, a tile 2.
   const long long rows_max = (long long)a.seqs.max_new * a.group, pieces = (rows_max + kRows - 1) / kRows;
   const long long span = a.window > 0 ? min((long long)a.seqs.max_len, (long long)a.window + a.seqs.max_new - 1) : a.seqs.max_len;

@@ -22,16 +22,15 @@
 //
 // Measured: 32 sequences of up to 32760 tokens, 40 heads on 8, bf16: 328 us (6.8 TB/s: the stream, a
 // little of it from L2); 64 sequences of up to 4608 tokens, 24 heads, e4m3: 159 us (5.9 TB/s).  More than 16 rows of an e4m3
-// pool are bound by latency between a warp's steps instead (30 rows 357 us where the stream takes 169; issue slots 41%,
+// pool are bound by latency between a warp's steps instead (30 rows 358 us where the stream takes 169; issue slots 41%,
 // tensor pipe 28%, 8 warps an SM): the warps of a key group convert the same codes, each for its row tile.
 //
 // bf16 pools: the type of V asks for bf16 weights.  At most 16 rows, a weight enters as two bf16 numbers, itself and
 // what rounding left over (16 bits), which costs nothing beside the stream (326.4 and 327.0 us above; the error against
 // float64 falls from 2.35e-3, the output's rounding and the weights', to 1.67e-3, the output's alone).  Above, where
-// the second product would cost 23% (30 rows) to 38% (60), weights are bf16, off by 2^-8 at most, and O is scaled by
-// the sum of the weights over the sum of the rounded ones, so that a row which one key dominates is not off by
-// that key's rounding (3% at 60 rows; second parts for the steps that count: 14 to 29%).  Where one key holds the weight
-// and others, of far larger values, the result, its rounding and theirs may add up, to 2^-7.  Sums are of the weights themselves.
+// the second product would cost 23% (30 rows) to 38% (60), weights are bf16, off by 2^-8 at most, and the maximum is
+// also moved where a key outweighs twice what its lane has of the row so far, so that a key which holds two thirds of a
+// row or more weighs exactly 1 and such a row is not off by its rounding (60 rows 548 -> 555 us).
 //
 // e4m3 pools: codes become fp16 exactly (one instruction for two), q becomes fp16 with a power of
 // two per row, also exactly, and a key's scales act on the logits: with x_j = s_j + e_j (e_j the
@@ -269,7 +268,7 @@ __device__ __forceinline__ size_t part_of(int block, int first) { return (size_t
 
 // The producer warp: follows the page table and fills the ring.  kJoin: a stage after each item's tiles
 // is left to the consumers, to join their results in.
-template <int D, bool kF8, bool kJoin, typename S>
+template <int D, bool kF8, bool kJoin, bool kCheck, typename S>
 __device__ __forceinline__ void produce(S& sm, const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p,
                                         FewWalk<Layout<D, kF8>::kTile>& w) {
   using L = Layout<D, kF8>;
@@ -295,7 +294,7 @@ __device__ __forceinline__ void produce(S& sm, const CUtensorMap& kmap, const CU
         const int pg = load_page(a.seqs, a.pool, w.b, pos);
         if (pg >= 0) row = (pg * a.pool.kv_heads + w.h) * a.pool.page + (pos & (a.pool.page - 1));
       }
-      if (ring >= kStages) ok = wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p);
+      if (ring >= kStages) ok = wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p) && !(kCheck && aborted(sm));
       // one vote for the pages (at most 8) and whether there is room, for all lanes what the last one saw
       const unsigned have = __ballot_sync(FULL, lane < 31 ? row >= 0 : !ok);
       ok = !(have >> 31);
@@ -321,7 +320,7 @@ __device__ __forceinline__ void produce(S& sm, const CUtensorMap& kmap, const CU
     skip = 0;
     if (kJoin && ok && w.t_begin < w.t_end) {
       const int st = ring % kStages;
-      if (ring >= kStages) ok = __all_sync(FULL, wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p));
+      if (ring >= kStages) ok = __all_sync(FULL, wait(sm, &sm.empty[st], (ring / kStages - 1) & 1, p) && !(kCheck && aborted(sm)));
       if (ok && lane == 0) mbar_arrive(&sm.full[st]);
       ring += ok;
     }
@@ -479,7 +478,7 @@ attn_row8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
   FewWalk<kTile> wk;
   if (!set_up<D, kF8>(sm, p, wk)) return;
   if (warp == 4) {
-    produce<D, kF8, true>(sm, kmap, vmap, p, wk);
+    produce<D, kF8, true, false>(sm, kmap, vmap, p, wk);
     return;
   }
   const int g = lane >> 2, q4 = lane & 3;
@@ -827,7 +826,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
   using L = Layout<D, kF8>;
   constexpr int kStages = L::kStages, kTile = L::kTile;
   constexpr int kKeyGroups = 4 / MT, kSteps = kTile / 16 / kKeyGroups;     // 16-key steps of a warp in a tile
-  constexpr bool kTwoParts = !kF8 && MT == 1, kRoundedSum = !kF8 && MT > 1;       // how bf16 weights enter P V
+  constexpr bool kTwoParts = !kF8 && MT == 1;                    // of bf16 weights
   extern __shared__ uint8_t smem_raw[];
   Smem<D, kF8>& sm = *reinterpret_cast<Smem<D, kF8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const AttnArgs& a = p.a;
@@ -835,7 +834,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
   FewWalk<kTile> wk;
   if (!set_up<D, kF8>(sm, p, wk)) return;
   if (warp == 4) {
-    produce<D, kF8, (kKeyGroups > 1)>(sm, kmap, vmap, p, wk);
+    produce<D, kF8, (kKeyGroups > 1), (MT > 1)>(sm, kmap, vmap, p, wk);
   } else {
     // =============================== consumers ===============================
     const int rt = warp % MT, kg = warp / MT;                 // row tile, key group
@@ -905,7 +904,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
       float acc[D / 8][4];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};      // lr: sum of the rounded weights
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
       for (int t = t_begin; t < t_end; ++t, ++ring) {
         const int st = ring % kStages;
@@ -971,10 +970,15 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
                 else s[n][x] = -INFINITY;
               }
           }
-          // ---- running maximum: moved only when a row outgrows it by 2^8 ----
+          // ---- running maximum: moved only when a row outgrows it by 2^8, or (bf16 in one part) twice what the lane has of it ----
+          float lag[2] = {kLazyLog2, kLazyLog2};
+          if constexpr (!kF8 && !kTwoParts) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) lag[e] = fminf(kLazyLog2, fmaxf(0.f, 1.f + __log2f(l[e])));
+          }
           const float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
           const float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-          if (__any_sync(FULL, x0 > m[0] + kLazyLog2 || x1 > m[1] + kLazyLog2)) {
+          if (__any_sync(FULL, x0 > m[0] + lag[0] || x1 > m[1] + lag[1])) {
             float mx[2] = {x0, x1}, f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -984,7 +988,6 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
               f[e] = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
               m[e] = mn;
               l[e] *= f[e];
-              if (kRoundedSum) lr[e] *= f[e];
             }
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
@@ -1015,7 +1018,6 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
               const int i = 2 * n + e;
               if constexpr (kTwoParts) split_bf16x2(w[n][2 * e], w[n][2 * e + 1], pa[i], pl[i]);
               else pa[i] = kF8 ? pack_f16x2(w[n][2 * e], w[n][2 * e + 1]) : pack_bf16x2(w[n][2 * e], w[n][2 * e + 1]);
-              if (kRoundedSum) lr[e] += __uint_as_float(pa[i] << 16) + __uint_as_float(pa[i] & 0xffff0000u);
             }
           // ---- O += P V ----
           uint32_t keep[2] = {FULL, FULL};                    // edge: my V rows (keys 2 q4, +1, and +8) that exist
@@ -1057,11 +1059,16 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
               }
             } else {
               ldsm4t(vb + chunk_at<D, false>(k0 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * c + (lane >> 4)), x);
+              if constexpr (kTwoParts) {
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t v0 = clean(x[2 * y], 0), v1 = clean(x[2 * y + 1], 1);
-                mma16816<false>(acc[2 * c + y], pa, v0, v1);
-                if constexpr (kTwoParts) mma16816<false>(acc[2 * c + y], pl, v0, v1);
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t v0 = clean(x[2 * y], 0), v1 = clean(x[2 * y + 1], 1);
+                  mma16816<false>(acc[2 * c + y], pa, v0, v1);
+                  mma16816<false>(acc[2 * c + y], pl, v0, v1);
+                }
+              } else {
+                mma16816<false>(acc[2 * c], pa, clean(x[0], 0), clean(x[1], 1));
+                mma16816<false>(acc[2 * c + 1], pa, clean(x[2], 0), clean(x[3], 1));
               }
             }
           }
@@ -1100,23 +1107,13 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
           else keys16(std::false_type(), k0);
         }
         __syncwarp();
-        if (lane == 0 && landed) mbar_arrive(&sm.empty[st]);
+        if (lane == 0 && (MT > 1 || landed)) mbar_arrive(&sm.empty[st]);
       }
       // ---- the row sums of the four lanes of a row, then the key groups ----
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         l[e] += __shfl_xor_sync(FULL, l[e], 1);
         l[e] += __shfl_xor_sync(FULL, l[e], 2);
-        if (kRoundedSum) {
-          lr[e] += __shfl_xor_sync(FULL, lr[e], 1);
-          lr[e] += __shfl_xor_sync(FULL, lr[e], 2);
-          const float c = lr[e] == 0.f ? 1.f : l[e] / lr[e];
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x) {
-            acc[x][2 * e] *= c;
-            acc[x][2 * e + 1] *= c;
-          }
-        }
       }
       if (kKeyGroups > 1) {
         const int st = ring % kStages;
@@ -1158,7 +1155,7 @@ attn_few(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUten
         }
         fence_async_shared();                                  // the stage goes back to TMA
         __syncwarp();
-        if (lane == 0 && landed) mbar_arrive(&sm.empty[st]);
+        if (lane == 0 && (MT > 1 || landed)) mbar_arrive(&sm.empty[st]);
         ++ring;
       }
 
