@@ -23,7 +23,7 @@
 // Measured: 32 sequences of up to 32760 tokens, 40 heads on 8, bf16: 328 us (6.8 TB/s: the stream, a
 // little of it from L2); 64 sequences of up to 4608 tokens, 24 heads, e4m3: 159 us (5.9 TB/s).  More than 16 rows of an e4m3
 // pool are bound by latency between a warp's steps instead (30 rows 358 us where the stream takes 169; issue slots 41%,
-// tensor pipe 28%, 8 warps an SM): the warps of a key group convert the same codes, each for its row tile.
+// tensor pipe 27%, 8 warps an SM): the warps of a key group convert the same codes, each for its row tile.
 //
 // bf16 pools: the type of V asks for bf16 weights.  At most 16 rows, a weight enters as two bf16 numbers, itself and
 // what rounding left over (16 bits), which costs nothing beside the stream (326.4 and 327.0 us above; the error against
