@@ -365,8 +365,8 @@ attn_chunk(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               };
               const bool first_half = t == t_first && hh == 0;
               if (!first_half) weights();
-              // bf16: no weight yet, or one that may dominate the row, or one that does not fit (NaN sums too)
-              if (__any_sync(FULL, kF8 ? first_half || ls > kRoom || m == -INFINITY : !(ls < fminf(kRoom, kPart * l)))) {
+              // bf16: no weight yet, or one that may dominate the row, or one that does not fit; rows of NaN stay as they are
+              if (__any_sync(FULL, kF8 ? first_half || ls > kRoom || m == -INFINITY : m == -INFINITY || ls > fminf(kRoom, kPart * l))) {
                 // rare but for the first half: move the maximum, and with it l and O
                 const float m_new = fmaxf(m, largest() * sl - kLift<kF8>);         // base-2 units
                 const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);         // 0 when m = -inf
