@@ -125,6 +125,19 @@ def test_a_row_that_one_late_key_dominates(dtype, new, d):
     assert bool(((got - ref).abs() <= bound).all()), ((got - ref).abs() / bound).max()
 
 
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("new,window,causal", [(4, 7, True), (7, 7, False), (30, 7, True), (30, 0, False), (8, 0, True)])
+def test_rows_of_few_keys_and_values_of_many_sizes(seed, new, window, causal):
+    """bf16 weights of 17 rows and more are off by 2^-8 each, not by that and what scaling a row would add."""
+    c = Case("bf16", 8, 1, 128, 16, [120, 41], [new, new], fill=False, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    for b in range(2):
+        c.k[b] = (c.k[b].float() * 2.0).bfloat16()
+        c.v[b] = (c.v[b].float() * torch.exp2(torch.rand(c.v[b].shape[:2], generator=g)[..., None] * 24 - 12)).bfloat16()
+    stored(c).check(causal, window)
+
+
 # ---- zeros in front of ordinary tokens (e4m3: a share's unit) ------------------------------------
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("zeros", [1, 127, 128, 130, 300, 699])
